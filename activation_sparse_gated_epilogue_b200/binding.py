@@ -82,6 +82,9 @@ def library() -> ctypes.CDLL:
             "hybrid_ffn_bwd": (I, [P, P, ctypes.POINTER(_SgeHybrid), P, P, P, P, P, P, P, P, I64, P,
                                    ctypes.c_size_t, P]),
             "sge_transpose_up_gate": (I, [P, P, P, I64, I64, P]),
+            "int8_quant_rows": (I, [P, I64, I64, I64, I, P, I64, P, P]),
+            "int8_linear": (I, [P, I64, P, P, I64, P, P, I64, I64, I64, I, P, P]),
+            "twell_gate_pack_int8": (I, [P, I64, P, P, I64, P, I64, I64, I64, I, I, P, P, P, P, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -456,3 +459,121 @@ def hybrid_ffn_bwd(x: torch.Tensor, dy: torch.Tensor, hy: Hybrid, wg_t: torch.Te
           _ptr(w_ug), _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd), d, _ptr(workspace),
           workspace.numel(), _stream(x.device, stream))
     return dx, dwg, dwu, dwd
+
+
+# ------------------------------------------------- 8-bit integer products
+
+
+def _launch(name: str, dev: torch.device, stream, *args) -> None:
+    """Call `name` with the stream appended, on the tensors' device."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, *args, _stream(dev, stream))
+    _call(name, *args, _stream(dev, stream))
+
+
+def _same_device(dev: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, x on {dev}")
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors allocated here but used on a stream other than the current
+    one: the allocator must not hand them out before that stream is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+@dataclass
+class Int8Rows:
+    """An 8-bit matrix: q int8 [rows][pitch] (pitch a multiple of 16, bytes
+    past `cols` are padding) and one fp32 scale per row.  Weights of E experts
+    are E blocks of rows."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    cols: int
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "Int8Rows":
+        return Int8Rows(torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=device),
+                        torch.empty(rows, dtype=torch.float32, device=device), cols)
+
+    @property
+    def rows(self) -> int:
+        return self.q.shape[0]
+
+    def _check(self, name: str, rows: Optional[int] = None, cols: Optional[int] = None) -> None:
+        q = _check(self.q, f"{name}.q", torch.int8)
+        if q.dim() != 2 or q.shape[1] % 16 or not 1 <= self.cols <= q.shape[1]:
+            raise ValueError(f"{name}.q must be [rows][pitch], pitch a multiple of 16, at least cols")
+        _check(self.scale, f"{name}.scale", torch.float32, (q.shape[0],))
+        if rows is not None and q.shape[0] != rows:
+            raise ValueError(f"{name} must have {rows} rows, got {q.shape[0]}")
+        if cols is not None and self.cols != cols:
+            raise ValueError(f"{name} must have {cols} columns, got {self.cols}")
+
+
+def int8_quant_rows(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None) -> Int8Rows:
+    """The rows of a bf16 or fp32 matrix as 8-bit integers with a scale each
+    (activations per token; weights per output channel, done once when they
+    are loaded).  x may be a row-strided view."""
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    n, d = x.shape
+    ldx = _check_rows(x, "x", x.dtype, (n, d))
+    if out is None:
+        out = Int8Rows.empty(n, d, x.device)
+        _used_on(stream, out.q, out.scale)
+    else:
+        out._check("out", n, d)
+        _same_device(x.device, out=out.q, scale=out.scale)
+    _launch("int8_quant_rows", x.device, stream, _ptr(x), ldx, n, d, _dtype_code(x), _ptr(out.q),
+            out.q.shape[1], _ptr(out.scale))
+    return out
+
+
+def int8_linear(xq: Int8Rows, wq: Int8Rows, dtype: torch.dtype = torch.bfloat16,
+                y: Optional[torch.Tensor] = None, diag: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """y[n][m] = (sum over k of xq[n][k] * wq[m][k]) * xq.scale[n] * wq.scale[m]
+    with exact integer sums, in bf16 or fp32."""
+    xq._check("xq")
+    wq._check("wq", cols=xq.cols)
+    n, m, dev = xq.rows, wq.rows, xq.q.device
+    if y is None:
+        y = torch.empty((n, m), dtype=dtype, device=dev)
+        _used_on(stream, y)
+    else:
+        _check(y, "y", dtype, (n, m))
+    if diag is not None:
+        _check(diag, "diag", torch.int32, (4,))
+    _same_device(dev, sx=xq.scale, wq=wq.q, sw=wq.scale, y=y, diag=diag)
+    _launch("int8_linear", dev, stream, _ptr(xq.q), xq.q.shape[1], _ptr(xq.scale), _ptr(wq.q),
+            wq.q.shape[1], _ptr(wq.scale), _ptr(y), n, m, xq.cols, _dtype_code(y), _ptr(diag))
+    return y
+
+
+def twell_gate_pack_int8(xq: Int8Rows, wg_q: Int8Rows, tile: int, cap: int, out: Optional[TwELL] = None,
+                         diag: Optional[torch.Tensor] = None, stream=None) -> TwELL:
+    """twell_gate_pack with the gate projection in 8-bit integers: TwELL
+    (bf16 values) of ReLU of int8_linear's product."""
+    xq._check("xq")
+    wg_q._check("wg_q", cols=xq.cols)
+    n, f, dev = xq.rows, wg_q.rows, xq.q.device
+    if out is None:
+        out = TwELL.empty(n, f, tile, cap, torch.bfloat16, dev)
+        _used_on(stream, out.count, out.idx, out.val)
+    else:
+        _check(out.count, "count", torch.uint8, (n, f // tile))
+        _check(out.idx, "idx", torch.uint8, (n, f // tile, cap))
+        _check(out.val, "val", torch.bfloat16, (n, f // tile, cap))
+    if diag is not None:
+        _check(diag, "diag", torch.int32, (4,))
+    _same_device(dev, sx=xq.scale, wg_q=wg_q.q, sw=wg_q.scale, count=out.count, idx=out.idx, val=out.val,
+                 diag=diag)
+    _launch("twell_gate_pack_int8", dev, stream, _ptr(xq.q), xq.q.shape[1], _ptr(xq.scale), _ptr(wg_q.q),
+            wg_q.q.shape[1], _ptr(wg_q.scale), n, xq.cols, f, tile, cap, _ptr(out.count), _ptr(out.idx),
+            _ptr(out.val), _ptr(diag))
+    return out

@@ -1,0 +1,487 @@
+// Persistent tcgen05 GEMM engine for 8-bit integers on sm_100a:
+//   D[r][c] = sum_k A[r][k] * B[c][k]   (int8 operands, K-major; exact int32
+//   accumulation in tensor memory, kind::i8)
+// with a pluggable epilogue, over one matrix or over groups of rows: with
+// `offsets` the rows [offsets[g], offsets[g+1]) of A multiply the g-th block
+// of p.n rows of B (the experts of a routed feed-forward block).  The integer
+// sums are exact, so results do not depend on the order of the k blocks.
+//
+// The roles, the stage ring, the bounded waits and the abort/drain protocol
+// are those of the bf16 engine (tc_gemm.cuh): warp 0 loads tiles by TMA
+// (128-byte swizzle rows = 128 int8), one thread of warp 1 issues the MMAs,
+// the other warps drain the accumulators.  PAIR: two CTAs on 256-row tiles
+// (cta_group::2), each loading its half of the operands; no multicast loads.
+//
+// PER_BLOCK: every 128-wide k block gets an accumulator of its own, which the
+// epilogue scales (one factor per row and k block) and adds in 32-bit floats:
+// the down projection of the feed-forward block, whose activations carry one
+// scale per token and 128 hidden units.
+#pragma once
+
+#include "i8_host.h"
+#include "sge_host.h"
+#include "tc_gemm.cuh"
+
+namespace sge {
+
+constexpr int kI8BK = 128;  // k per stage: one 128-byte swizzle row
+constexpr int kMaxGroups = 256;
+constexpr int64_t kI8MaxK = 133000;        // k * 127 * 127 stays below 2^31
+constexpr int64_t kI8MaxRows = 1LL << 30;  // row and column indices of a tile stay 32-bit
+
+template <int BN_, int NB_, int NACC_, int HALVES_, bool PAIR_, bool PER_BLOCK_ = false>
+struct I8Shape {
+  static constexpr int BN = BN_, NB = NB_, NACC = NACC_, HALVES = HALVES_;
+  static constexpr bool PAIR = PAIR_, PER_BLOCK = PER_BLOCK_;
+  static constexpr int THREADS = 64 + 128 * HALVES;
+  static constexpr int BM = PAIR ? 2 * kBM : kBM;
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of each B tile this CTA loads
+  static constexpr int A_BYTES = kBM * kI8BK;
+  static constexpr int B_BYTES = B_ROWS * kI8BK;
+  static constexpr int STAGE_BYTES = A_BYTES + NB * B_BYTES;
+  static constexpr int STAGES = (196 * 1024) / STAGE_BYTES > 8 ? 8 : (196 * 1024) / STAGE_BYTES;
+  static constexpr int ACC_COLS = BN * NB;
+  static constexpr int USED_COLS = NACC * ACC_COLS;
+  static constexpr int TMEM_COLS = USED_COLS <= 32 ? 32 : USED_COLS <= 64 ? 64 : USED_COLS <= 128 ? 128
+                                   : USED_COLS <= 256 ? 256 : 512;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 /*align slack*/ + 512 /*barriers*/;
+  static_assert(USED_COLS <= 512, "TMEM columns");
+  static_assert(BN % (PAIR ? 32 : 16) == 0 && BN <= 256, "UMMA N");
+  static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "1024-byte aligned sub-tiles");
+  static_assert(HALVES == 1 || NB == 1, "column halves need one accumulator");
+  static_assert(!PER_BLOCK || NB == 1, "per-block scales: one accumulator");
+};
+
+struct I8Problem {
+  int rows;    // rows of A
+  int n;       // output columns of a group (rows of B per group)
+  int k;       // bytes of a row
+  int groups;  // 1..kMaxGroups
+  int splits;  // K is cut into this many parts, each an output of its own
+  const int32_t* offsets;  // [groups + 1] row bounds on the device, or null (one group)
+};
+
+// One output tile: rows [row0, row_end) (at most BM of them are computed),
+// columns [col0, col0 + BN) of group `group`, k blocks [kb0, kb1).
+struct I8Tile {
+  int group, row0, row_end, col0, split, kb0, kb1;
+};
+
+// The tile list, built in shared memory from the group bounds.
+template <class Shape>
+struct I8Sched {
+  int off[kMaxGroups + 1];    // clamped group bounds
+  int first[kMaxGroups + 1];  // row blocks before group g
+
+  // one whole warp
+  __device__ __forceinline__ void build(const I8Problem& p, int lane) {
+    int run = 0, floor = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+      const int g = g0 + lane;
+      // group g ends at hi and begins where the one before ends; bounds that
+      // are out of range or out of order give fewer rows, never an overlap or
+      // an access out of range
+      int hi = p.rows, begin = 0;
+      if (p.offsets) {
+        hi = g < p.groups ? min(max(p.offsets[g + 1], 0), p.rows) : 0;
+        if (g == 0) begin = min(max(p.offsets[0], 0), p.rows);
+        hi = max(hi, max(begin, floor));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, hi, o);
+          if (lane >= o) hi = max(hi, u);
+        }
+      }
+      int lo = __shfl_up_sync(0xffffffffu, hi, 1);
+      if (lane == 0) lo = g == 0 ? begin : floor;
+      floor = __shfl_sync(0xffffffffu, hi, 31);
+      const int blocks = g < p.groups ? (hi - lo + Shape::BM - 1) / Shape::BM : 0;
+      int incl = blocks;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      if (g < p.groups) {
+        off[g] = lo;
+        first[g] = run + incl - blocks;
+        if (g == p.groups - 1) off[p.groups] = hi;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) first[p.groups] = run;
+  }
+
+  __device__ __forceinline__ I8Tile tile(const I8Problem& p, int t, int k_blocks) const {
+    I8Tile r;
+    r.split = t % p.splits;
+    t /= p.splits;
+    const int m_blocks = first[p.groups];
+    const int mb = t % m_blocks;
+    r.col0 = t / m_blocks * Shape::BN;
+    int lo = 0, hi = p.groups;  // the last group whose first block is <= mb
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= mb) lo = mid;
+      else hi = mid;
+    }
+    r.group = lo;
+    r.row0 = off[lo] + (mb - first[lo]) * Shape::BM;
+    r.row_end = off[lo + 1];
+    const int per = (k_blocks + p.splits - 1) / p.splits;
+    r.kb0 = min(k_blocks, r.split * per);
+    r.kb1 = min(k_blocks, r.kb0 + per);
+    return r;
+  }
+
+  __device__ __forceinline__ int tiles(const I8Problem& p) const {
+    return first[p.groups] * ((p.n + Shape::BN - 1) / Shape::BN) * p.splits;
+  }
+};
+
+// Instruction descriptor: kind::i8, signed A and B, 32-bit integer
+// accumulator, both operands K-major, tile M x N.
+constexpr uint32_t umma_idesc_i8(int m, int n) {
+  return (2u << 4)                                // D format: s32
+         | (1u << 7)                              // A format: signed 8 bit
+         | (1u << 10)                             // B format: signed 8 bit
+         | (static_cast<uint32_t>(n >> 3) << 17)  // N / 8
+         | (static_cast<uint32_t>(m >> 4) << 24); // M / 16
+}
+
+template <bool PAIR>
+SGE_DEV void umma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+template <bool PAIR>
+SGE_DEV void i8_commit(uint64_t* bar) {
+  if constexpr (PAIR) umma2_commit_mc(bar, 0x3);
+  else umma_commit(bar);
+}
+
+// What an epilogue call gets: the accumulator's TMEM address (this warp's
+// lanes, its first column), this thread's row and its tile.
+struct I8Out {
+  uint32_t taddr;
+  int64_t row;  // row of A of this thread
+  bool row_ok;  // inside the tile's group
+  int col0;     // first column (within the group) of this warp's share
+  int group, split;
+};
+
+// W floats of one row to out (rounded to its type), of which `left` lie inside
+// the row; `pitch` (elements) tells whether 16-byte stores are aligned.
+template <int W>
+SGE_DEV void store_cols(__nv_bfloat16* out, const float (&v)[W], int left, int pitch) {
+  if (left >= W && pitch % 8 == 0) {
+#pragma unroll
+    for (int j = 0; j < W; j += 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = static_cast<uint32_t>(f32_to_bf16_bits(v[j + 2 * i])) |
+               (static_cast<uint32_t>(f32_to_bf16_bits(v[j + 2 * i + 1])) << 16);
+      *reinterpret_cast<uint4*>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (j < left) out[j] = __float2bfloat16_rn(v[j]);
+  }
+}
+template <int W>
+SGE_DEV void store_cols(float* out, const float (&v)[W], int left, int pitch) {
+  if (left >= W && pitch % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < W; j += 4)
+      *reinterpret_cast<float4*>(out + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (j < left) out[j] = v[j];
+  }
+}
+
+template <class Shape, class Epilogue>
+__global__ void __launch_bounds__(Shape::THREADS, 1)
+    i8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
+                   const __grid_constant__ CUtensorMap map_b1, const I8Problem p, const Epilogue epi,
+                   int32_t* diag) {
+  constexpr int BN = Shape::BN, NB = Shape::NB, NACC = Shape::NACC, STAGES = Shape::STAGES;
+  constexpr bool PAIR = Shape::PAIR, PER_BLOCK = Shape::PER_BLOCK;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ I8Sched<Shape> sched;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * Shape::STAGE_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tmem_full = empty + STAGES;
+  uint64_t* tmem_empty = tmem_full + NACC;
+  uint64_t* drain = tmem_empty + NACC;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+  const bool leader = rank == 0;
+  const int worker = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int n_workers = PAIR ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < NACC; ++a) {
+      mbar_init(&tmem_full[a], 1);
+      mbar_init(&tmem_empty[a], (PAIR ? 8 : 4) * Shape::HALVES);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&map_a);
+    tma_prefetch_desc(&map_b0);
+    if (NB == 2) tma_prefetch_desc(&map_b1);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(tmem_holder, Shape::TMEM_COLS);
+    else tmem_alloc(tmem_holder, Shape::TMEM_COLS);
+  }
+  // the set-up above overlaps the previous kernel; what it wrote (the group
+  // bounds among it) is read only below
+  grid_dep_wait();
+  grid_dep_launch();
+  if (warp == 0) sched.build(p, lane);
+  tc_fence_before();
+  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote arrive / TMA
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int k_blocks = (p.k + kI8BK - 1) / kI8BK;
+  const int num_tiles = sched.tiles(p);
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, armed = 0, armed_par = 0;
+      const uint32_t bytes =
+          PAIR ? 2 * Shape::STAGE_BYTES : a_box_rows(p.rows) * kI8BK + NB * Shape::B_BYTES;
+      for (int t = worker; t < num_tiles && !*abort_flag; t += n_workers) {
+        const I8Tile tc = sched.tile(p, t, k_blocks);
+        const int a_row = tc.row0 + static_cast<int>(rank) * kBM;
+        const int b_row = tc.group * p.n + tc.col0 + static_cast<int>(rank) * Shape::B_ROWS;
+        for (int kb = tc.kb0; kb < tc.kb1; ++kb) {
+          if (!wait_or_abort(&empty[s], ph ^ 1, abort_flag, diag)) break;
+          uint8_t* sa = smem + s * Shape::STAGE_BYTES;
+          if (leader) mbar_arrive_expect_tx(&full[s], bytes);
+          if constexpr (PAIR) {
+            tma_load_2d_pair(sa, &map_a, &full[s], kb * kI8BK, a_row);
+            tma_load_2d_pair(sa + Shape::A_BYTES, &map_b0, &full[s], kb * kI8BK, b_row);
+            if (NB == 2)
+              tma_load_2d_pair(sa + Shape::A_BYTES + Shape::B_BYTES, &map_b1, &full[s], kb * kI8BK, b_row);
+          } else {
+            tma_load_2d(sa, &map_a, &full[s], kb * kI8BK, a_row);
+            tma_load_2d(sa + Shape::A_BYTES, &map_b0, &full[s], kb * kI8BK, b_row);
+            if (NB == 2)
+              tma_load_2d(sa + Shape::A_BYTES + Shape::B_BYTES, &map_b1, &full[s], kb * kI8BK, b_row);
+          }
+          armed |= 1u << s;
+          armed_par = (armed_par & ~(1u << s)) | (ph << s);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // Drain: no load of this CTA (PAIR: of either CTA) is in flight after this.
+      if (leader)
+        for (int t = 0; t < STAGES; ++t)
+          if (armed & (1u << t)) mbar_wait(&full[t], (armed_par >> t) & 1, diag);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc = umma_idesc_i8(Shape::BM, BN);
+      int s = 0, acc = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true;
+      for (int t = worker; ok && t < num_tiles && !*abort_flag; t += n_workers) {
+        const I8Tile tc = sched.tile(p, t, k_blocks);
+        for (int kb = tc.kb0; kb < tc.kb1; ++kb) {
+          const bool fresh = PER_BLOCK || kb == tc.kb0;
+          if (fresh) {
+            ok = wait_or_abort(&tmem_empty[acc], acc_ph ^ 1, abort_flag, diag);
+            if (!ok) break;
+          }
+          ok = wait_or_abort(&full[s], ph, abort_flag, diag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * Shape::ACC_COLS;
+          const uint32_t sa = smem_u32(smem + s * Shape::STAGE_BYTES);
+#pragma unroll
+          for (int k = 0; k < kI8BK / 32; ++k) {
+            const uint64_t adesc = umma_desc_sw128(sa + k * 32);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const uint64_t bdesc = umma_desc_sw128(sa + Shape::A_BYTES + b * Shape::B_BYTES + k * 32);
+              umma_i8<PAIR>(d_tmem + b * BN, adesc, bdesc, idesc, (!fresh || k != 0) ? 1u : 0u);
+            }
+          }
+          i8_commit<PAIR>(&empty[s]);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (PER_BLOCK || kb == tc.kb1 - 1) {
+            i8_commit<PAIR>(&tmem_full[acc]);
+            if (++acc == NACC) {
+              acc = 0;
+              acc_ph ^= 1;
+            }
+          }
+        }
+      }
+      i8_commit<PAIR>(drain);  // completes once every MMA issued above has
+    }
+    if (lane == 0) mbar_wait(drain, 0, diag);
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------- epilogue
+    const int quarter = warp & 3;      // TMEM lanes this warp may access
+    const int half = (warp - 2) >> 2;  // column half (HALVES = 2)
+    constexpr int COLS = BN / Shape::HALVES;
+    const uint32_t lane_base = tmem_base + half * COLS + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t release0 = PAIR ? mapa_shared(smem_u32(&tmem_empty[0]), 0) : 0;
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    const auto release = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(release0 + acc * 8);
+        else mbar_arrive(&tmem_empty[acc]);
+      }
+      if (++acc == NACC) {
+        acc = 0;
+        acc_ph ^= 1;
+      }
+    };
+    bool ok = true;
+    for (int t = worker; ok && t < num_tiles; t += n_workers) {
+      const I8Tile tc = sched.tile(p, t, k_blocks);
+      if (tc.kb0 >= tc.kb1) continue;  // an empty split (the epilogue's reader skips it too)
+      I8Out o;
+      o.row = static_cast<int64_t>(tc.row0) + rank * kBM + quarter * 32 + lane;
+      o.row_ok = o.row < tc.row_end;
+      o.col0 = tc.col0 + half * COLS;
+      o.group = tc.group;
+      o.split = tc.split;
+      if constexpr (PER_BLOCK) {
+        float sum[COLS];
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) sum[j] = 0.0f;
+        float scale = epi.block_scale(o, tc.kb0);
+        for (int kb = tc.kb0; kb < tc.kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(&tmem_full[acc], acc_ph, abort_flag, diag));
+          if (!ok) break;
+          tc_fence_after();
+          const float s = scale;
+          if (kb + 1 < tc.kb1) scale = epi.block_scale(o, kb + 1);  // in flight during this block
+#pragma unroll
+          for (int ch = 0; ch < COLS / 32; ++ch) {
+            uint32_t r[32];
+            tmem_ld32(lane_base + acc * Shape::ACC_COLS + ch * 32, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              sum[ch * 32 + j] = fmaf(__int2float_rn(static_cast<int>(r[j])), s, sum[ch * 32 + j]);
+          }
+          release();
+        }
+        if (ok) epi.template store<COLS>(o, sum, p.n);
+      } else {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&tmem_full[acc], acc_ph, abort_flag, diag));
+        if (!ok) break;
+        tc_fence_after();
+        o.taddr = lane_base + acc * Shape::ACC_COLS;
+        epi.template run<COLS>(o, p.n);
+        release();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // no CTA leaves while its pair may still touch its barriers or TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, Shape::TMEM_COLS);
+    else tmem_dealloc(tmem_base, Shape::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------- launchers
+
+// Tensor maps of an engine call.  B: `b_rows` rows of k bytes, pitch ldb.
+struct I8Maps {
+  CUtensorMap a, b0, b1;
+};
+
+template <class Shape>
+int make_i8_maps(I8Maps* m, const I8Problem& p, const int8_t* a, int64_t lda, const int8_t* b0,
+                 const int8_t* b1, int64_t ldb) {
+  const uint32_t a_box = Shape::PAIR ? kBM : a_box_rows(p.rows);
+  const uint64_t b_rows = static_cast<uint64_t>(p.n) * p.groups;
+  int rc = make_tmap_i8(&m->a, a, p.rows, p.k, lda, a_box);
+  if (!rc) rc = make_tmap_i8(&m->b0, b0, b_rows, p.k, ldb, Shape::B_ROWS);
+  if (!rc) rc = make_tmap_i8(&m->b1, b1 ? b1 : b0, b_rows, p.k, ldb, Shape::B_ROWS);
+  return rc;
+}
+
+// `max_m_blocks`: the most row blocks the call can have (with groups: their
+// rows rounded up), for the grid.
+template <class Shape, class Epi>
+int launch_i8_gemm(const I8Maps& m, const I8Problem& p, const Epi& epi, int32_t* diag, cudaStream_t st,
+                   const char* what) {
+  auto kern = i8_gemm_kernel<Shape, Epi>;
+  int rc = set_smem_limit(reinterpret_cast<const void*>(kern), Shape::SMEM_BYTES);
+  if (rc) return rc;
+  int64_t m_blocks = (p.rows + Shape::BM - 1) / Shape::BM;
+  if (p.offsets) m_blocks += p.groups - 1 < p.rows ? p.groups - 1 : p.rows;  // at most: one partial block a group
+  const int64_t tiles = m_blocks * ((p.n + Shape::BN - 1) / Shape::BN) * p.splits;
+  const int64_t slots = Shape::PAIR ? sm_count() / 2 : sm_count();
+  const int workers = static_cast<int>(tiles < slots ? tiles : slots);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(Shape::PAIR ? 2 * workers : workers);
+  cfg.blockDim = dim3(Shape::THREADS);
+  cfg.dynamicSmemBytes = Shape::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = Shape::PAIR ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m.a, m.b0, m.b1, p, epi, diag);
+  if (e != cudaSuccess) return fail(SGE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
+}
+
+}  // namespace sge

@@ -436,6 +436,58 @@ int hybrid_ffn_bwd(const void* x, const void* dy, const sge_hybrid* hy, const vo
 int sge_transpose_up_gate(const void* wu_t, const void* wg_t, void* w_ug, int64_t d_ff,
                           int64_t d_model, void* stream);
 
+/*
+ * 8-bit integer products with a scale for each token and each channel.
+ *
+ * A quantised matrix is int8 rows with one fp32 scale per row; the rows'
+ * pitch is a multiple of 16 bytes.  Value (r, c) stands for q[r][c] * scale[r].
+ * Activations have one row per token, weights one row per output channel
+ * (neuron-major, as above); weights are quantised once, when they are loaded.
+ *
+ * int8_quant_rows -- quantises the rows of x:
+ *   amax = max |x|,  scale = amax / 127,  q = rint(x * (127 / amax)),
+ * each operation in fp32, rounded to nearest even.  A row whose amax is below
+ * 2^-100 becomes zeros with scale 0; a row that holds an infinity or a NaN
+ * becomes zeros with scale NaN, so that its products are NaN.
+ *   x      [n_rows][n_cols]  SGE_BF16 or SGE_F32, row pitch ldx elements;
+ *          any n_cols (rows of 16-byte vectors that are 16-byte aligned are
+ *          read as such, others element by element)
+ *   q      int8 [n_rows][ldq]: columns n_cols .. ldq-1 are set to 0
+ *   scale  fp32 [n_rows]
+ * Errors: SGE_ERR_ARG for sizes below 0 (n_cols below 1), ldx < n_cols,
+ * ldq < n_cols or ldq % 16; SGE_ERR_UNSUPPORTED for other dtypes.
+ */
+int int8_quant_rows(const void* x, int64_t ldx, int64_t n_rows, int64_t n_cols, int dtype, int8_t* q,
+                    int64_t ldq, float* scale, void* stream);
+
+/*
+ * int8_linear -- y[n][m] = (sum_k xq[n][k] * wq[m][k]) * sx[n] * sw[m].
+ * The sums are exact (tcgen05 with 32-bit integer accumulation); they are
+ * converted to fp32, multiplied by sx, then by sw, each rounded to nearest
+ * even, and once more to a bf16 y.
+ *   xq  int8 [n_tokens][ldx], sx fp32 [n_tokens]
+ *   wq  int8 [n_out][ldw],    sw fp32 [n_out]
+ *   y   [n_tokens][n_out]  dtype (SGE_BF16 or SGE_F32), contiguous; any n_out
+ * Bytes n_in .. ldx-1 (ldw-1) of a row are not part of the product.
+ * Errors: SGE_ERR_ARG for bad sizes or pitches (ldx, ldw: multiples of 16, at
+ * least n_in); SGE_ERR_UNSUPPORTED for n_in > 133000 (the sums would pass 32
+ * bits), sizes of 2^30 and more, other dtypes.
+ */
+int int8_linear(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* wq, int64_t ldw, const float* sw,
+                void* y, int64_t n_tokens, int64_t n_out, int64_t n_in, int dtype, int32_t* diag, void* stream);
+
+/*
+ * twell_gate_pack_int8 -- twell_gate_pack with an 8-bit gate projection:
+ *   g[n][j] = (sum_k xq[n][k] * wg_q[j][k]) * sx[n] * sw[j]   (as int8_linear)
+ * and TwELL of the g > 0, values rounded to bf16.  Its output feeds
+ * twell_hybrid_up_down, twell_fused_up_down and hybrid_pack like
+ * twell_gate_pack's.  Tile widths, capacities, overflow counts and untouched
+ * slots as there; operands, limits and errors as int8_linear's.
+ */
+int twell_gate_pack_int8(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* wg_q, int64_t ldw,
+                         const float* sw, int64_t n_tokens, int64_t d_model, int64_t d_ff, int tile, int cap,
+                         uint8_t* count, uint8_t* idx, void* val, int32_t* diag, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

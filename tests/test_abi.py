@@ -209,3 +209,72 @@ def test_transpose_up_gate_rejects_bad_arguments(lib):
     assert b"null" in lib.sge_last_error()
     assert lib.sge_transpose_up_gate(ctypes.c_void_p(4100), p, p, 128, 64, None) == 1
     assert b"aligned" in lib.sge_last_error()
+
+
+def _quant(lib, **kw):
+    p = ctypes.c_void_p(4096)
+    a = dict(x=p, ldx=64, rows=8, cols=64, dt=sge.SGE_BF16, q=p, ldq=64, scale=p)
+    a.update(kw)
+    return lib.int8_quant_rows(a["x"], a["ldx"], a["rows"], a["cols"], a["dt"], a["q"], a["ldq"], a["scale"], None)
+
+
+def test_int8_quant_rejects_bad_arguments(lib):
+    assert _quant(lib, rows=0, x=None, q=None, scale=None) == 0
+    assert _quant(lib, rows=-1) == 1
+    assert _quant(lib, cols=0) == 1
+    assert _quant(lib, dt=7) == 2
+    assert _quant(lib, ldx=63) == 1
+    assert b"ldx" in lib.sge_last_error()
+    assert _quant(lib, ldq=72) == 1
+    assert _quant(lib, ldq=48) == 1
+    assert b"ldq" in lib.sge_last_error()
+    assert _quant(lib, q=None) == 1
+    assert b"null" in lib.sge_last_error()
+    assert _quant(lib, scale=ctypes.c_void_p(4098)) == 1
+    assert b"aligned" in lib.sge_last_error()
+    assert _quant(lib, rows=1 << 31) == 2
+
+
+def _linear(lib, **kw):
+    p = ctypes.c_void_p(4096)
+    a = dict(xq=p, ldx=64, sx=p, wq=p, ldw=64, sw=p, y=p, n=8, m=32, k=64, dt=sge.SGE_BF16, diag=None)
+    a.update(kw)
+    return lib.int8_linear(a["xq"], a["ldx"], a["sx"], a["wq"], a["ldw"], a["sw"], a["y"], a["n"], a["m"],
+                           a["k"], a["dt"], a["diag"], None)
+
+
+def test_int8_linear_rejects_bad_arguments(lib):
+    assert _linear(lib, n=0, xq=None, y=None) == 0
+    assert _linear(lib, n=-1) == 1
+    assert _linear(lib, m=0) == 1
+    assert _linear(lib, k=0) == 1
+    assert _linear(lib, dt=2) == 2
+    assert _linear(lib, k=65) == 1                     # pitch below the row
+    assert _linear(lib, ldx=72) == 1
+    assert _linear(lib, ldw=68) == 1
+    assert b"pitches" in lib.sge_last_error()
+    assert _linear(lib, k=133001, ldx=1 << 18, ldw=1 << 18) == 2
+    assert b"32-bit sums" in lib.sge_last_error()
+    assert _linear(lib, n=1 << 30) == 2
+    assert _linear(lib, sw=None) == 1
+    assert _linear(lib, y=None) == 1
+    assert _linear(lib, y=ctypes.c_void_p(4104)) == 1
+    assert b"aligned" in lib.sge_last_error()
+
+
+def test_twell_gate_pack_int8_rejects_bad_arguments(lib):
+    p = ctypes.c_void_p(4096)
+
+    def call(n=8, d=64, f=256, ld=64, tile=128, cap=128, xq=p, count=p, idx=p, val=p):
+        return lib.twell_gate_pack_int8(xq, ld, p, p, ld, p, n, d, f, tile, cap, count, idx, val, None, None)
+
+    assert call(n=0, xq=None, count=None) == 0
+    assert call(tile=48, cap=48) == 2
+    assert call(f=200) == 1
+    assert call(cap=0) == 1
+    assert call(cap=129) == 1
+    assert call(d=65) == 1                             # pitch
+    assert call(xq=None) == 1
+    assert call(val=None) == 1
+    assert call(idx=ctypes.c_void_p(4097)) == 1
+    assert call(d=200000, ld=200000) == 2

@@ -12,6 +12,7 @@ from .binding import (  # noqa: F401
     fused_workspace, Hybrid, hybrid_pack, hybrid_ffn_fwd, hybrid_fwd_workspace,
     hybrid_ffn_bwd, hybrid_bwd_workspace, interleave_up_down, twell_hybrid_up_down, routed_workspace,
     transpose_up_gate, debug_flags, Int8Rows, int8_quant_rows, int8_linear, twell_gate_pack_int8,
+    MoeRoute, moe_route_fwd, moe_route_bwd, moe_route_workspace,
 )
 
 __all__ = [
@@ -21,4 +22,5 @@ __all__ = [
     "hybrid_ffn_bwd", "hybrid_bwd_workspace", "interleave_up_down", "twell_hybrid_up_down",
     "routed_workspace", "transpose_up_gate", "debug_flags",
     "Int8Rows", "int8_quant_rows", "int8_linear", "twell_gate_pack_int8",
+    "MoeRoute", "moe_route_fwd", "moe_route_bwd", "moe_route_workspace",
 ]

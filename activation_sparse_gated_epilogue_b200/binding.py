@@ -84,6 +84,9 @@ def library() -> ctypes.CDLL:
             "sge_transpose_up_gate": (I, [P, P, P, I64, I64, P]),
             "int8_quant_rows": (I, [P, I64, I64, I64, I, P, I64, P, P]),
             "int8_linear": (I, [P, I64, P, P, I64, P, P, I64, I64, I64, I, P, P]),
+            "moe_route_workspace_bytes": (ctypes.c_size_t, [I64, I]),
+            "moe_route_fwd": (I, [P, P, I64, I, I, I, I, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
+            "moe_route_bwd": (I, [P, P, I64, I, I, I, I, P, P, P, P, P, P, P, P, P]),
             "twell_gate_pack_int8": (I, [P, I64, P, P, I64, P, I64, I64, I64, I, I, P, P, P, P, P]),
         }
         for name, (res, args) in sigs.items():
@@ -576,4 +579,107 @@ def twell_gate_pack_int8(xq: Int8Rows, wg_q: Int8Rows, tile: int, cap: int, out:
     _launch("twell_gate_pack_int8", dev, stream, _ptr(xq.q), xq.q.shape[1], _ptr(xq.scale), _ptr(wg_q.q),
             wg_q.q.shape[1], _ptr(wg_q.scale), n, xq.cols, f, tile, cap, _ptr(out.count), _ptr(out.idx),
             _ptr(out.val), _ptr(diag))
+    return out
+
+
+# ------------------------------------------------------------ expert router
+
+
+@dataclass
+class MoeRoute:
+    """What moe_route_fwd gives (see include/sge.h): ids, w, pos [N][k]; order
+    [N * k]; counts [E]; offsets [E + 1]; loss, n_live [1]; and the settings
+    that its gradient needs again."""
+    ids: torch.Tensor
+    w: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    pos: torch.Tensor
+    order: torch.Tensor
+    loss: torch.Tensor
+    n_live: torch.Tensor
+    renorm: bool = True
+
+    @staticmethod
+    def empty(n_tokens: int, n_experts: int, top_k: int, device) -> "MoeRoute":
+        i = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)  # noqa: E731
+        f = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)  # noqa: E731
+        return MoeRoute(i(n_tokens, top_k), f(n_tokens, top_k), i(n_experts), i(n_experts + 1),
+                        i(n_tokens, top_k), i(n_tokens * top_k), f(1), i(1))
+
+    def _check(self, n: int, e: int, k: int, dev) -> None:
+        for name, dt, shape in (("ids", torch.int32, (n, k)), ("w", torch.float32, (n, k)),
+                                ("counts", torch.int32, (e,)), ("offsets", torch.int32, (e + 1,)),
+                                ("pos", torch.int32, (n, k)), ("order", torch.int32, (n * k,)),
+                                ("loss", torch.float32, (1,)), ("n_live", torch.int32, (1,))):
+            t = _check(getattr(self, name), name, dt, shape)
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, the logits on {dev}")
+
+
+def moe_route_workspace(n_tokens: int, n_experts: int, top_k: int, device) -> torch.Tensor:
+    """Scratch for moe_route_fwd (each block's counts and probability sums)."""
+    nbytes = library().moe_route_workspace_bytes(n_tokens, n_experts)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _check_logits(logits: torch.Tensor, mask: Optional[torch.Tensor]):
+    _check(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens][experts]")
+    if mask is not None:
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise ValueError(f"mask must be uint8 or bool, got {mask.dtype}")
+        _check(mask, "mask", None, (logits.shape[0],))
+        _same_device(logits.device, mask=mask)
+    return logits.shape
+
+
+def moe_route_fwd(logits: torch.Tensor, top_k: int, renorm: bool = True, mask: Optional[torch.Tensor] = None,
+                  out: Optional[MoeRoute] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> MoeRoute:
+    """Top-k experts and weights of each token, assignments per expert, their
+    expert order, and the balance loss.  ``mask`` [N]: 0 for padding tokens."""
+    n, e = _check_logits(logits, mask)
+    dev = logits.device
+    if out is None:
+        out = MoeRoute.empty(n, e, max(top_k, 0), dev)
+        _used_on(stream, out.ids, out.w, out.counts, out.offsets, out.pos, out.order, out.loss, out.n_live)
+    else:
+        out._check(n, e, top_k, dev)
+    out.renorm = bool(renorm)
+    if workspace is None:
+        workspace = moe_route_workspace(n, e, top_k, dev)
+        _used_on(stream, workspace)
+    else:
+        _check(workspace, "workspace", torch.uint8)
+        _same_device(dev, workspace=workspace)
+    _launch("moe_route_fwd", dev, stream, _ptr(logits), _ptr(mask), n, e, top_k, int(out.renorm),
+            _dtype_code(logits), _ptr(out.ids), _ptr(out.w), _ptr(out.counts), _ptr(out.offsets), _ptr(out.pos),
+            _ptr(out.order), _ptr(out.loss), _ptr(out.n_live), _ptr(workspace), workspace.numel())
+    return out
+
+
+def moe_route_bwd(logits: torch.Tensor, route: MoeRoute, dloss: Optional[torch.Tensor] = None,
+                  dw: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dlogits from the gradients of the balance loss (fp32 [1]) and of the
+    weights (fp32 [N][k]); logits and mask as in the forward that gave route."""
+    n, e = _check_logits(logits, mask)
+    dev = logits.device
+    k = route.ids.shape[1]
+    route._check(n, e, k, dev)
+    if dloss is not None:
+        _check(dloss, "dloss", torch.float32, (1,))
+    if dw is not None:
+        _check(dw, "dw", torch.float32, (n, k))
+    if out is None:
+        out = torch.empty_like(logits)
+        _used_on(stream, out)
+    else:
+        _check(out, "out", logits.dtype, (n, e))
+    _same_device(dev, dloss=dloss, dw=dw, out=out)
+    _launch("moe_route_bwd", dev, stream, _ptr(logits), _ptr(mask), n, e, k, int(route.renorm),
+            _dtype_code(logits), _ptr(route.ids), _ptr(route.w), _ptr(route.counts), _ptr(route.offsets),
+            _ptr(route.n_live), _ptr(dloss), _ptr(dw), _ptr(out))
     return out

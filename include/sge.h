@@ -488,6 +488,50 @@ int twell_gate_pack_int8(const int8_t* xq, int64_t ldx, const float* sx, const i
                          const float* sw, int64_t n_tokens, int64_t d_model, int64_t d_ff, int tile, int cap,
                          uint8_t* count, uint8_t* idx, void* val, int32_t* diag, void* stream);
 
+/*
+ * moe_route_fwd -- the router of a mixture of feed-forward experts.  From the
+ * logits of a token's experts: p = softmax(logits); ids = its top_k largest
+ * logits in descending order (a tie goes to the lower index); weights
+ *   w[n][j] = p[ids[n][j]]                       renorm == 0
+ *   w[n][j] = softmax over the chosen logits     renorm != 0
+ * and over all tokens
+ *   counts[e]   assignments of expert e          offsets[e]  their prefix sums
+ *   pos[n][j]   the place of assignment (n, j) in expert order: expert by
+ *               expert, tokens ascending within one; order[pos] = n * top_k + j
+ *   loss        E * sum_e (counts[e] / sum counts) * (mean over live tokens of p_e)
+ * A token is live unless its mask byte is 0 (its logits are then not read) or
+ * all its logits are -infinity.  An expert whose logit is -infinity is never
+ * chosen.  Where no expert is left, ids and pos are -1 and w is 0; order is -1
+ * behind the last assignment.  A live token with a NaN or +infinity among its
+ * logits is routed nowhere and makes the loss NaN.
+ *   logits   [N][E]  SGE_BF16 or SGE_F32          mask  uint8 [N] or NULL (all live)
+ *   ids, pos int32 [N][top_k]    w  fp32 [N][top_k]    order  int32 [N * top_k]
+ *   counts   int32 [E]   offsets  int32 [E + 1]   loss  fp32 [1]   n_live  int32 [1]
+ * The results do not depend on scheduling (integers: exact; sums in a fixed
+ * order).  Limits (SGE_ERR_UNSUPPORTED beyond): E <= 256, top_k <= 16,
+ * N * top_k < 2^30.  The workspace (256-byte aligned) is used by this call alone.
+ */
+size_t moe_route_workspace_bytes(int64_t n_tokens, int n_experts);
+int moe_route_fwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int n_experts, int top_k,
+                  int renorm, int dtype, int32_t* ids, float* w, int32_t* counts, int32_t* offsets, int32_t* pos,
+                  int32_t* order, float* loss, int32_t* n_live, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/*
+ * moe_route_bwd -- the gradient of moe_route_fwd's loss and weights with
+ * respect to the logits (ids and counts are constants):
+ *   dp_e = dloss * E * (counts[e] / sum counts) / live tokens  [+ dw at ids, renorm == 0]
+ *   dlogits = p (dp - <p, dp>)   [+ w_j (dw_j - <w, dw>) at ids_j, renorm != 0]
+ * mask, ids, w, counts, offsets and n_live as given to and by moe_route_fwd;
+ * dloss fp32 [1] on the device or NULL (0); dw fp32 [N][top_k] or NULL (0;
+ * entries whose id is -1 are not read).  dlogits [N][E] in the logits' dtype:
+ * 0 for tokens that are not live, NaN for live ones that are not finite.
+ */
+int moe_route_bwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int n_experts, int top_k,
+                  int renorm, int dtype, const int32_t* ids, const float* w, const int32_t* counts,
+                  const int32_t* offsets, const int32_t* n_live, const float* dloss, const float* dw,
+                  void* dlogits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -278,3 +278,40 @@ def test_twell_gate_pack_int8_rejects_bad_arguments(lib):
     assert call(val=None) == 1
     assert call(idx=ctypes.c_void_p(4097)) == 1
     assert call(d=200000, ld=200000) == 2
+
+
+def _route(lib, bwd=False, **kw):
+    p = ctypes.c_void_p(4096)
+    a = dict(logits=p, mask=None, n=100, e=16, k=2, dt=sge.SGE_F32, ids=p, w=p, counts=p, offsets=p, pos=p,
+             order=p, loss=p, live=p, ws=p, ws_bytes=1 << 30, dlogits=p)
+    a.update(kw)
+    head = (a["logits"], a["mask"], a["n"], a["e"], a["k"], 1, a["dt"], a["ids"], a["w"], a["counts"], a["offsets"])
+    if bwd:
+        return lib.moe_route_bwd(*head, a["live"], None, None, a["dlogits"], None)
+    return lib.moe_route_fwd(*head, a["pos"], a["order"], a["loss"], a["live"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_moe_route_rejects_bad_arguments(lib, bwd):
+    assert _route(lib, bwd, n=-1) == 1
+    assert _route(lib, bwd, e=0) == 1
+    assert _route(lib, bwd, k=0) == 1
+    assert _route(lib, bwd, k=17) == 1                 # above E
+    assert _route(lib, bwd, e=300) == 2
+    assert _route(lib, bwd, e=64, k=17) == 2
+    assert _route(lib, bwd, dt=5) == 2
+    assert _route(lib, bwd, n=1 << 29) == 2
+    assert _route(lib, bwd, logits=None) == 1
+    assert _route(lib, bwd, counts=None) == 1
+    assert b"null" in lib.sge_last_error()
+    assert _route(lib, bwd, ids=ctypes.c_void_p(4100)) == 1
+    assert b"aligned" in lib.sge_last_error()
+    if bwd:
+        assert _route(lib, bwd, n=0, logits=None) == 0
+    else:
+        need = lib.moe_route_workspace_bytes(100, 16)
+        assert need > 0 and need % 256 == 0
+        assert _route(lib, ws_bytes=need - 1) == 1
+        assert b"workspace" in lib.sge_last_error()
+        assert _route(lib, ws=ctypes.c_void_p(4096 + 16)) == 1
+        assert lib.moe_route_workspace_bytes(100, 257) == 0

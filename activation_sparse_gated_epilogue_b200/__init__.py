@@ -13,6 +13,7 @@ from .binding import (  # noqa: F401
     hybrid_ffn_bwd, hybrid_bwd_workspace, interleave_up_down, twell_hybrid_up_down, routed_workspace,
     transpose_up_gate, debug_flags, Int8Rows, int8_quant_rows, int8_linear, twell_gate_pack_int8,
     MoeRoute, moe_route_fwd, moe_route_bwd, moe_route_workspace,
+    int8_ffn_fwd, moe_int8_ffn_fwd, int8_ffn_workspace,
 )
 
 __all__ = [
@@ -23,4 +24,5 @@ __all__ = [
     "routed_workspace", "transpose_up_gate", "debug_flags",
     "Int8Rows", "int8_quant_rows", "int8_linear", "twell_gate_pack_int8",
     "MoeRoute", "moe_route_fwd", "moe_route_bwd", "moe_route_workspace",
+    "int8_ffn_fwd", "moe_int8_ffn_fwd", "int8_ffn_workspace",
 ]

@@ -87,6 +87,9 @@ def library() -> ctypes.CDLL:
             "moe_route_workspace_bytes": (ctypes.c_size_t, [I64, I]),
             "moe_route_fwd": (I, [P, P, I64, I, I, I, I, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
             "moe_route_bwd": (I, [P, P, I64, I, I, I, I, P, P, P, P, P, P, P, P, P]),
+            "int8_ffn_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I, I, I]),
+            "int8_ffn_fwd": (I, [P] * 8 + [I64, I64, I64, I, P, ctypes.c_size_t, P, P]),
+            "moe_int8_ffn_fwd": (I, [P] * 11 + [I64, I64, I64, I, I, I, P, ctypes.c_size_t, P, P]),
             "twell_gate_pack_int8": (I, [P, I64, P, P, I64, P, I64, I64, I64, I, I, P, P, P, P, P]),
         }
         for name, (res, args) in sigs.items():
@@ -683,3 +686,73 @@ def moe_route_bwd(logits: torch.Tensor, route: MoeRoute, dloss: Optional[torch.T
             _dtype_code(logits), _ptr(route.ids), _ptr(route.w), _ptr(route.counts), _ptr(route.offsets),
             _ptr(route.n_live), _ptr(dloss), _ptr(dw), _ptr(out))
     return out
+
+
+# --------------------------------------- feed-forward block on 8-bit weights
+
+
+def int8_ffn_workspace(n_tokens: int, d_model: int, d_ff: int, n_experts: int, top_k: int, dtype: torch.dtype,
+                       device) -> torch.Tensor:
+    """Scratch for int8_ffn_fwd (n_experts = top_k = 1) and moe_int8_ffn_fwd."""
+    nbytes = library().int8_ffn_workspace_bytes(n_tokens, d_model, d_ff, n_experts, top_k, _DTYPES[dtype])
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _ffn_args(x, wg_q, wu_q, wd_t_q, e, k, y, workspace, diag, stream):
+    """Checked operands of the two calls: (n, d, f, y, workspace)."""
+    _check(x, "x")
+    n, d = x.shape
+    dev = x.device
+    if wg_q.rows % e:
+        raise ValueError(f"wg_q must have a multiple of {e} rows, got {wg_q.rows}")
+    f = wg_q.rows // e
+    for name, m, rows, cols in (("wg_q", wg_q, e * f, d), ("wu_q", wu_q, e * f, d), ("wd_t_q", wd_t_q, e * d, f)):
+        m._check(name, rows, cols)
+        if m.q.shape[1] != (cols + 15) // 16 * 16:
+            raise ValueError(f"{name}.q must have rows of {(cols + 15) // 16 * 16} bytes, got {m.q.shape[1]}")
+    if y is None:
+        y = torch.empty_like(x)
+        _used_on(stream, y)
+    else:
+        _check(y, "y", x.dtype, (n, d))
+    if workspace is None:
+        workspace = int8_ffn_workspace(n, d, f, e, k, x.dtype, dev)
+        _used_on(stream, workspace)
+    else:
+        _check(workspace, "workspace", torch.uint8)
+    if diag is not None:
+        _check(diag, "diag", torch.int32, (4,))
+    _same_device(dev, wg_q=wg_q.q, sg=wg_q.scale, wu_q=wu_q.q, su=wu_q.scale, wd_t_q=wd_t_q.q, sd=wd_t_q.scale,
+                 y=y, workspace=workspace, diag=diag)
+    return n, d, f, y, workspace
+
+
+def int8_ffn_fwd(x: torch.Tensor, wg_q: Int8Rows, wu_q: Int8Rows, wd_t_q: Int8Rows,
+                 y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 diag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gated feed-forward block on 8-bit weights.  ``wd_t_q`` is
+    int8_quant_rows of W_down transposed, [d][F]."""
+    n, d, f, y, workspace = _ffn_args(x, wg_q, wu_q, wd_t_q, 1, 1, y, workspace, diag, stream)
+    _launch("int8_ffn_fwd", x.device, stream, _ptr(x), _ptr(wg_q.q), _ptr(wg_q.scale), _ptr(wu_q.q),
+            _ptr(wu_q.scale), _ptr(wd_t_q.q), _ptr(wd_t_q.scale), _ptr(y), n, d, f, _dtype_code(x),
+            _ptr(workspace), workspace.numel(), _ptr(diag))
+    return y
+
+
+def moe_int8_ffn_fwd(x: torch.Tensor, wg_q: Int8Rows, wu_q: Int8Rows, wd_t_q: Int8Rows, w: torch.Tensor,
+                     offsets: torch.Tensor, pos: torch.Tensor, y: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, diag: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """The experts' blocks on 8-bit weights (expert by expert in the rows of
+    wg_q, wu_q and wd_t_q), each token's summed with its weights; w, offsets
+    and pos are moe_route_fwd's."""
+    e, k = offsets.shape[0] - 1, w.shape[1]
+    n, d, f, y, workspace = _ffn_args(x, wg_q, wu_q, wd_t_q, e, k, y, workspace, diag, stream)
+    _check(w, "w", torch.float32, (n, k))
+    _check(offsets, "offsets", torch.int32, (e + 1,))
+    _check(pos, "pos", torch.int32, (n, k))
+    _same_device(x.device, w=w, offsets=offsets, pos=pos)
+    _launch("moe_int8_ffn_fwd", x.device, stream, _ptr(x), _ptr(wg_q.q), _ptr(wg_q.scale), _ptr(wu_q.q),
+            _ptr(wu_q.scale), _ptr(wd_t_q.q), _ptr(wd_t_q.scale), _ptr(w), _ptr(offsets), _ptr(pos), _ptr(y), n, d,
+            f, e, k, _dtype_code(x), _ptr(workspace), workspace.numel(), _ptr(diag))
+    return y

@@ -1,0 +1,375 @@
+// The gated feed-forward block on 8-bit weights, of one expert or of the
+// experts that a route chose:
+//
+//   xq, sx    the tokens' rows, quantised (int8_quant_rows), in expert order
+//   g, u      (sum xq wg) * sx * sg  and  (sum xq wu) * sx * su, fp32
+//   h         ReLU(g) * u, quantised per token and group of 128 hidden units
+//   z         sum over groups of (sum hq wd) * sh, times sd
+//   y         z, or the sum of a token's experts' z with its weights
+//
+// The hidden activation's scale is per token and 128 hidden units, not per
+// token, because a whole row's largest value is known only when every column
+// tile of the first product is done: that would take a wider copy of h to
+// HBM and back.  128 units are one tile of the first product's epilogue and
+// one k block of the second product, whose integer sums over a block are
+// exact; the blocks are scaled and added in fp32.
+#include "i8_gemm.cuh"
+#include "i8_quant.cuh"
+
+namespace sge {
+
+constexpr int kHGroup = 128;  // hidden units that share a scale
+
+// ------------------------------------------- quantise and order the tokens
+
+// One warp per token; its row goes to every place of the token (pos null: to
+// its own row).
+template <class T>
+__global__ void __launch_bounds__(256) i8_dispatch_kernel(const T* __restrict__ x, int64_t n, int d, int k,
+                                                          const int32_t* __restrict__ pos, int rows,
+                                                          int8_t* __restrict__ q, int64_t ldq,
+                                                          float* __restrict__ scale) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= n) return;
+  // place j of the token, or a number outside [0, rows)
+  const auto place = [&](int j) -> uint32_t {
+    return pos ? static_cast<uint32_t>(__ldg(pos + row * k + j)) : static_cast<uint32_t>(row);
+  };
+  uint32_t amax;
+  quant_row<T, true, 8>(x + row * d, d, lane, amax, [&](int c, const auto& f, float inv) {
+    for (int j = 0; j < k; ++j) {
+      const uint32_t p = place(j);
+      if (p < static_cast<uint32_t>(rows)) store_q(q + p * ldq + c, f, inv);
+    }
+  });
+  const float s = quant_scale(amax).scale;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t p = place(j);
+    if (p >= static_cast<uint32_t>(rows)) continue;
+    if (lane == 0) scale[p] = s;
+    // a row ends with at most 8 bytes of padding (d % 8 == 0)
+    if (lane == 1 && d % 16) *reinterpret_cast<uint2*>(q + p * ldq + d) = make_uint2(0, 0);
+  }
+}
+
+// --------------------------------------------------------------- epilogues
+
+// h = ReLU(g) * u of one row and 128 hidden units, quantised.
+struct EpiI8Gated {
+  int8_t* hq;
+  int64_t ldh;
+  float* hs;  // [groups of 128][rows]
+  int64_t rows;
+  const float* sx;
+  const float* sg;
+  const float* su;
+
+  template <int COLS>
+  __device__ __forceinline__ void run(const I8Out& o, int n) const {
+    static_assert(COLS == kHGroup, "a tile's columns are one group");
+    const float s = o.row_ok ? __ldg(sx + o.row) : 0.0f;
+    const float* cg = sg + static_cast<int64_t>(o.group) * n + o.col0;
+    const float* cu = su + static_cast<int64_t>(o.group) * n + o.col0;
+    float h[COLS];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int ch = 0; ch < COLS / 32; ++ch) {
+      uint32_t g[32], u[32];
+      tmem_ld32(o.taddr + ch * 32, g);
+      tmem_ld32(o.taddr + COLS + ch * 32, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        // n % 8 == 0: four columns are inside the group's weights or all outside
+        const bool in = o.col0 + ch * 32 + j < n;
+        const float4 a = in ? __ldg(reinterpret_cast<const float4*>(cg + ch * 32 + j)) : make_float4(0, 0, 0, 0);
+        const float4 b = in ? __ldg(reinterpret_cast<const float4*>(cu + ch * 32 + j)) : make_float4(0, 0, 0, 0);
+        const float sa[4] = {a.x, a.y, a.z, a.w}, sb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float gv = __int2float_rn(static_cast<int>(g[j + i])) * s * sa[i];
+          const float uv = __int2float_rn(static_cast<int>(u[j + i])) * s * sb[i];
+          // a NaN (from a token that is not finite) stays one
+          const float v = in ? (gv < 0.0f ? 0.0f : gv) * uv : 0.0f;
+          h[ch * 32 + j + i] = v;
+          amax = max(amax, abs_bits(v));
+        }
+      }
+    }
+    if (!o.row_ok) return;
+    const QuantScale qs = quant_scale(amax);
+    int8_t* dst = hq + o.row * ldh + o.col0;
+#pragma unroll
+    for (int j = 0; j < COLS; j += 16)
+      if (o.col0 + j < ldh)
+        *reinterpret_cast<uint4*>(dst + j) = make_uint4(
+            quant_pack4(h[j], h[j + 1], h[j + 2], h[j + 3], qs.inv),
+            quant_pack4(h[j + 4], h[j + 5], h[j + 6], h[j + 7], qs.inv),
+            quant_pack4(h[j + 8], h[j + 9], h[j + 10], h[j + 11], qs.inv),
+            quant_pack4(h[j + 12], h[j + 13], h[j + 14], h[j + 15], qs.inv));
+    hs[static_cast<int64_t>(o.col0 / kHGroup) * rows + o.row] = qs.scale;
+  }
+};
+
+template <class T>
+struct EpiI8Down {
+  T* z;  // [splits][rows][n]
+  int64_t rows;
+  const float* hs;
+  const float* sd;
+
+  __device__ __forceinline__ float block_scale(const I8Out& o, int kb) const {
+    return o.row_ok ? hs[static_cast<int64_t>(kb) * rows + o.row] : 0.0f;
+  }
+
+  template <int COLS>
+  __device__ __forceinline__ void store(const I8Out& o, const float (&sum)[COLS], int n) const {
+    if (!o.row_ok) return;
+    const float* cd = sd + static_cast<int64_t>(o.group) * n + o.col0;
+    T* out = z + (o.split * rows + o.row) * n + o.col0;
+#pragma unroll
+    for (int j = 0; j < COLS; j += 8) {
+      if (o.col0 + j >= n) break;  // n % 8 == 0
+      const float4 a = __ldg(reinterpret_cast<const float4*>(cd + j));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(cd + j + 4));
+      const float v[8] = {sum[j] * a.x,     sum[j + 1] * a.y, sum[j + 2] * a.z, sum[j + 3] * a.w,
+                          sum[j + 4] * b.x, sum[j + 5] * b.y, sum[j + 6] * b.z, sum[j + 7] * b.w};
+      store_cols<8>(out + j, v, 8, 8);
+    }
+  }
+};
+
+// y[t] = sum over the token's places of w * (sum over splits of z), in the
+// order of the token's experts and of the splits.  Z: the type z is kept in.
+// Whole sums (one split) are kept in the activations' type, which rounds a
+// bf16 result once per expert and once in the end: half the bytes of fp32.
+template <class T, class Z>
+__global__ void __launch_bounds__(256) i8_combine_kernel(const Z* __restrict__ z, int rows, int splits, int64_t n,
+                                                         int d, int k, const float* __restrict__ w,
+                                                         const int32_t* __restrict__ pos, T* __restrict__ y) {
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int W = 8;
+  const int per_row = d / W;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= n * per_row) return;
+  const int64_t t = i / per_row;
+  const int c = static_cast<int>(i % per_row) * W;
+  float sum[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) sum[j] = 0.0f;
+  for (int a = 0; a < k; ++a) {
+    const uint32_t p = pos ? static_cast<uint32_t>(__ldg(pos + t * k + a)) : static_cast<uint32_t>(t);
+    if (p >= static_cast<uint32_t>(rows)) continue;
+    const float wt = w ? __ldg(w + t * k + a) : 1.0f;
+    float part[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) part[j] = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+      const Z* src = z + (static_cast<int64_t>(s) * rows + p) * d + c;
+#pragma unroll
+      for (int j = 0; j < W; j += Vec16<Z>::N) {
+        float f[Vec16<Z>::N];
+        Vec16<Z>::unpack(*reinterpret_cast<const uint4*>(src + j), f);
+#pragma unroll
+        for (int m = 0; m < Vec16<Z>::N; ++m) part[j + m] += f[m];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) sum[j] = fmaf(wt, part[j], sum[j]);
+  }
+  store_cols<W>(y + t * d + c, sum, W, W);
+}
+
+// ------------------------------------------------------------------- host
+
+static int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
+
+struct FfnPlan {
+  int64_t rows;     // assignments: n, or n * k
+  bool pairs;       // CTA-pair tiles
+  int splits;       // parts of the down projection's K
+  bool combine;     // y is summed from z by the combine kernel
+  bool z_f32;
+  int64_t ldx, ldh;
+  size_t xq, sx, hq, hs, z, total;  // workspace offsets
+};
+
+using GateUpPair = I8Shape<128, 2, 2, 1, true>;
+using GateUpOne = I8Shape<128, 2, 2, 1, false>;
+using DownPair = I8Shape<256, 1, 2, 2, true, true>;
+using DownOne = I8Shape<128, 1, 4, 1, false, true>;
+
+static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype, bool routed) {
+  FfnPlan p = {};
+  p.rows = routed ? n * k : n;
+  // 256-row tiles when an expert has more rows than that on average
+  p.pairs = p.rows / e > 256;
+  p.splits = 1;
+  const int64_t kb = (f + kI8BK - 1) / kI8BK;
+  if (!p.pairs) {
+    // few output tiles: cut K so that about every SM (of 148) has one, at
+    // least 4 blocks (512 hidden units) each, no part empty
+    const int64_t groups = e < p.rows ? e : p.rows;  // experts that can have rows
+    const int64_t tiles = (p.rows / kBM + groups) * ((d + DownOne::BN - 1) / DownOne::BN);
+    int64_t s = tiles ? 148 / tiles : 1;
+    if (s > kb / 4) s = kb / 4;
+    if (s > 16) s = 16;
+    if (s < 1) s = 1;
+    const int64_t per = (kb + s - 1) / s;
+    p.splits = static_cast<int>((kb + per - 1) / per);
+  }
+  p.combine = routed || p.splits > 1;
+  p.z_f32 = p.splits > 1 || dtype == SGE_F32;
+  p.ldx = round16(d);
+  p.ldh = round16(f);
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  p.xq = take(static_cast<size_t>(p.rows) * p.ldx);
+  p.sx = take(static_cast<size_t>(p.rows) * 4);
+  p.hq = take(static_cast<size_t>(p.rows) * p.ldh);
+  p.hs = take(static_cast<size_t>(p.rows) * kb * 4);
+  p.z = p.combine ? take(static_cast<size_t>(p.rows) * p.splits * d * (p.z_f32 ? 4 : 2)) : 0;
+  p.total = at;
+  return p;
+}
+
+struct FfnArgs {
+  const void* x;
+  const int8_t *wg, *wu, *wd;
+  const float *sg, *su, *sd;
+  const float* w;
+  const int32_t *offsets, *pos;
+  void* y;
+  int64_t n, d, f;
+  int e, k;
+  uint8_t* ws;
+  int32_t* diag;
+  cudaStream_t st;
+};
+
+template <class Shape, class Z>
+static int ffn_down(const FfnArgs& a, const FfnPlan& p, const I8Problem& pr, Z* z) {
+  I8Maps m;
+  const int rc = make_i8_maps<Shape>(&m, pr, reinterpret_cast<int8_t*>(a.ws + p.hq), p.ldh, a.wd, nullptr, p.ldh);
+  if (rc) return rc;
+  const EpiI8Down<Z> epi{z, p.rows, reinterpret_cast<float*>(a.ws + p.hs), a.sd};
+  return launch_i8_gemm<Shape>(m, pr, epi, a.diag, a.st, "int8 ffn (down)");
+}
+
+template <class Shape>
+static int ffn_gate_up(const FfnArgs& a, const FfnPlan& p, const I8Problem& pr) {
+  I8Maps m;
+  const int rc = make_i8_maps<Shape>(&m, pr, reinterpret_cast<int8_t*>(a.ws + p.xq), p.ldx, a.wg, a.wu, p.ldx);
+  if (rc) return rc;
+  const EpiI8Gated epi{reinterpret_cast<int8_t*>(a.ws + p.hq), p.ldh, reinterpret_cast<float*>(a.ws + p.hs), p.rows,
+                       reinterpret_cast<float*>(a.ws + p.sx), a.sg, a.su};
+  return launch_i8_gemm<Shape>(m, pr, epi, a.diag, a.st, "int8 ffn (gate, up)");
+}
+
+template <class T, class Z>
+static int ffn_combine(const FfnArgs& a, const FfnPlan& p) {
+  const int64_t threads = a.n * (a.d / 8);
+  return launch_pdl(i8_combine_kernel<T, Z>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, a.st,
+                    "int8 ffn (combine)", reinterpret_cast<const Z*>(a.ws + p.z), static_cast<int>(p.rows), p.splits,
+                    a.n, static_cast<int>(a.d), a.k, a.w, a.pos, static_cast<T*>(a.y));
+}
+
+template <class T>
+static int ffn(const FfnArgs& a, const FfnPlan& p) {
+  int rc = launch_pdl(i8_dispatch_kernel<T>, dim3(static_cast<unsigned>((a.n + 7) / 8)), dim3(256), 0, a.st,
+                      "int8 ffn (quantise)", static_cast<const T*>(a.x), a.n, static_cast<int>(a.d), a.k, a.pos,
+                      static_cast<int>(p.rows), reinterpret_cast<int8_t*>(a.ws + p.xq), p.ldx,
+                      reinterpret_cast<float*>(a.ws + p.sx));
+  if (rc) return rc;
+  const I8Problem up{static_cast<int>(p.rows), static_cast<int>(a.f), static_cast<int>(a.d), a.e, 1, a.offsets};
+  const I8Problem down{static_cast<int>(p.rows), static_cast<int>(a.d), static_cast<int>(a.f), a.e, p.splits, a.offsets};
+  rc = p.pairs ? ffn_gate_up<GateUpPair>(a, p, up) : ffn_gate_up<GateUpOne>(a, p, up);
+  if (rc) return rc;
+  if (!p.combine) {
+    T* y = static_cast<T*>(a.y);
+    return p.pairs ? ffn_down<DownPair>(a, p, down, y) : ffn_down<DownOne>(a, p, down, y);
+  }
+  if (p.z_f32) {
+    float* z = reinterpret_cast<float*>(a.ws + p.z);
+    rc = p.pairs ? ffn_down<DownPair>(a, p, down, z) : ffn_down<DownOne>(a, p, down, z);
+    return rc ? rc : ffn_combine<T, float>(a, p);
+  }
+  T* z = reinterpret_cast<T*>(a.ws + p.z);
+  rc = p.pairs ? ffn_down<DownPair>(a, p, down, z) : ffn_down<DownOne>(a, p, down, z);
+  return rc ? rc : ffn_combine<T, T>(a, p);
+}
+
+static int check_ffn_sizes(const char* fn, int64_t n, int64_t d, int64_t f, int e, int k, int dtype) {
+  if (n < 0 || d < 1 || f < 1 || e < 1 || k < 1 || k > e)
+    return fail(SGE_ERR_ARG, "%s: bad sizes N=%lld d=%lld F=%lld E=%d k=%d", fn, (long long)n, (long long)d,
+                (long long)f, e, k);
+  if (d % 8 || f % 8) return fail(SGE_ERR_ARG, "%s: d_model and d_ff must be multiples of 8", fn);
+  if (dtype != SGE_BF16 && dtype != SGE_F32) return fail(SGE_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+  if (e > kMaxGroups || k > 16) return fail(SGE_ERR_UNSUPPORTED, "%s: more than %d experts, or top_k above 16", fn, kMaxGroups);
+  if (d > kI8MaxK) return fail(SGE_ERR_UNSUPPORTED, "%s: d_model beyond %lld (the 32-bit sums' bound)", fn, (long long)kI8MaxK);
+  if (n >= kI8MaxRows / k || f >= kI8MaxRows / e || d >= kI8MaxRows / e)
+    return fail(SGE_ERR_UNSUPPORTED, "%s: size beyond 2^30", fn);
+  return SGE_OK;
+}
+
+static int run_ffn(const char* fn, FfnArgs a, int dtype, bool routed, void* workspace, size_t workspace_bytes) {
+  const int rc = check_ffn_sizes(fn, a.n, a.d, a.f, a.e, a.k, dtype);
+  if (rc) return rc;
+  if (a.n == 0) return SGE_OK;
+  if (!a.x || !a.wg || !a.sg || !a.wu || !a.su || !a.wd || !a.sd || !a.y || !workspace ||
+      (routed && (!a.w || !a.offsets || !a.pos)))
+    return fail(SGE_ERR_ARG, "%s: null pointer", fn);
+  if (!aligned16(a.x) || !aligned16(a.wg) || !aligned16(a.sg) || !aligned16(a.wu) || !aligned16(a.su) ||
+      !aligned16(a.wd) || !aligned16(a.sd) || !aligned16(a.y) || !aligned16(a.w) || !aligned16(a.offsets) ||
+      !aligned16(a.pos) || !aligned16(a.diag) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(SGE_ERR_ARG, "%s: pointer not 16-byte aligned (workspace: 256)", fn);
+  const FfnPlan p = ffn_plan(a.n, a.d, a.f, a.e, a.k, dtype, routed);
+  if (workspace_bytes < p.total)
+    return fail(SGE_ERR_ARG, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, p.total);
+  a.ws = static_cast<uint8_t*>(workspace);
+  return dtype == SGE_BF16 ? ffn<__nv_bfloat16>(a, p) : ffn<float>(a, p);
+}
+
+}  // namespace sge
+
+using namespace sge;
+
+extern "C" size_t int8_ffn_workspace_bytes(int64_t n_tokens, int64_t d_model, int64_t d_ff, int n_experts, int top_k,
+                                           int dtype) {
+  if (check_ffn_sizes("int8_ffn_workspace_bytes", n_tokens, d_model, d_ff, n_experts, top_k, dtype)) return 0;
+  // int8_ffn_fwd and moe_int8_ffn_fwd both take it
+  const size_t routed = ffn_plan(n_tokens, d_model, d_ff, n_experts, top_k, dtype, true).total;
+  const size_t dense = ffn_plan(n_tokens, d_model, d_ff, n_experts, top_k, dtype, false).total;
+  return n_experts > 1 || routed > dense ? routed : dense;
+}
+
+extern "C" int int8_ffn_fwd(const void* x, const int8_t* wg_q, const float* sg, const int8_t* wu_q, const float* su,
+                            const int8_t* wd_q, const float* sd, void* y, int64_t n_tokens, int64_t d_model,
+                            int64_t d_ff, int dtype, void* workspace, size_t workspace_bytes, int32_t* diag,
+                            void* stream) {
+  NvtxRange nvtx_range("int8_ffn_fwd");
+  clear_error();
+  const FfnArgs a = {x, wg_q, wu_q, wd_q, sg, su, sd, nullptr, nullptr, nullptr, y, n_tokens, d_model, d_ff, 1, 1,
+                     nullptr, diag, static_cast<cudaStream_t>(stream)};
+  return run_ffn("int8_ffn_fwd", a, dtype, false, workspace, workspace_bytes);
+}
+
+extern "C" int moe_int8_ffn_fwd(const void* x, const int8_t* wg_q, const float* sg, const int8_t* wu_q,
+                                const float* su, const int8_t* wd_q, const float* sd, const float* w,
+                                const int32_t* offsets, const int32_t* pos, void* y, int64_t n_tokens,
+                                int64_t d_model, int64_t d_ff, int n_experts, int top_k, int dtype, void* workspace,
+                                size_t workspace_bytes, int32_t* diag, void* stream) {
+  NvtxRange nvtx_range("moe_int8_ffn_fwd");
+  clear_error();
+  const FfnArgs a = {x, wg_q, wu_q, wd_q, sg, su, sd, w, offsets, pos, y, n_tokens, d_model, d_ff, n_experts, top_k,
+                     nullptr, diag, static_cast<cudaStream_t>(stream)};
+  return run_ffn("moe_int8_ffn_fwd", a, dtype, true, workspace, workspace_bytes);
+}

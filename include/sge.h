@@ -532,6 +532,48 @@ int moe_route_bwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int
                   const int32_t* offsets, const int32_t* n_live, const float* dloss, const float* dw,
                   void* dlogits, void* stream);
 
+/*
+ * int8_ffn_fwd -- the gated feed-forward block on 8-bit weights (dense_ffn_fwd's
+ * formula).  Each token's row of x is quantised as by int8_quant_rows;
+ *   g, u  as int8_linear of the rows with wg_q and wu_q, in fp32
+ *   h     = ReLU(g) * u (fp32), quantised by the same rule in groups of 128
+ *           hidden units of a token (the last group may be shorter)
+ *   y     = sum over groups of (exact integer sum of hq * wd_q) * (group's
+ *           scale), in fp32, times sd, rounded to dtype
+ * A token whose row holds an infinity or a NaN gets NaN.
+ *   x, y  [N][d]  dtype (SGE_BF16 or SGE_F32)
+ *   wg_q, wu_q  int8 [F][d rounded up to 16]   sg, su  fp32 [F]
+ *   wd_q  int8 [d][F rounded up to 16]         sd      fp32 [d]
+ *         (W_down transposed: one row and scale per output channel)
+ *
+ * moe_int8_ffn_fwd -- the same with n_experts blocks, of which each token
+ * takes those that moe_route_fwd chose:
+ *   y[n] = sum_j w[n][j] * block_{ids[n][j]}(x[n])
+ *   wg_q, wu_q  int8 [E][F][.], sg, su [E][F];  wd_q  int8 [E][d][.], sd [E][d]
+ *   w fp32 [N][top_k], offsets int32 [E + 1], pos int32 [N][top_k] as given by
+ *   moe_route_fwd.  A place of -1 adds nothing; a token without places gets
+ *   y = 0.  Places and bounds outside [0, N * top_k] are left out, never
+ *   followed.  Each expert's weights are read only if it has tokens.
+ *   An expert's y is rounded to dtype before the weighted sum when dtype is
+ *   SGE_BF16 and the product's K was not split.
+ *
+ * Results do not depend on scheduling.  The workspace (256-byte aligned,
+ * int8_ffn_workspace_bytes for either call; n_experts = top_k = 1 for
+ * int8_ffn_fwd) belongs to one call at a time.
+ * Errors: SGE_ERR_ARG for bad sizes, d % 8, F % 8, top_k > E, a workspace too
+ * small; SGE_ERR_UNSUPPORTED for d > 133000, E > 256, top_k > 16, other
+ * dtypes, N * top_k, E * F or E * d of 2^30 and more.
+ */
+size_t int8_ffn_workspace_bytes(int64_t n_tokens, int64_t d_model, int64_t d_ff, int n_experts, int top_k,
+                                int dtype);
+int int8_ffn_fwd(const void* x, const int8_t* wg_q, const float* sg, const int8_t* wu_q, const float* su,
+                 const int8_t* wd_q, const float* sd, void* y, int64_t n_tokens, int64_t d_model, int64_t d_ff,
+                 int dtype, void* workspace, size_t workspace_bytes, int32_t* diag, void* stream);
+int moe_int8_ffn_fwd(const void* x, const int8_t* wg_q, const float* sg, const int8_t* wu_q, const float* su,
+                     const int8_t* wd_q, const float* sd, const float* w, const int32_t* offsets,
+                     const int32_t* pos, void* y, int64_t n_tokens, int64_t d_model, int64_t d_ff, int n_experts,
+                     int top_k, int dtype, void* workspace, size_t workspace_bytes, int32_t* diag, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -315,3 +315,46 @@ def test_moe_route_rejects_bad_arguments(lib, bwd):
         assert b"workspace" in lib.sge_last_error()
         assert _route(lib, ws=ctypes.c_void_p(4096 + 16)) == 1
         assert lib.moe_route_workspace_bytes(100, 257) == 0
+
+
+def _ffn(lib, routed, **kw):
+    p = ctypes.c_void_p(4096)
+    a = dict(x=p, wg=p, sg=p, w=p, offsets=p, pos=p, y=p, n=10, d=64, f=128, e=4, k=2, dt=sge.SGE_BF16, ws=p,
+             ws_bytes=1 << 40)
+    a.update(kw)
+    head = (a["x"], a["wg"], a["sg"], p, p, p, p)
+    tail = (a["dt"], a["ws"], a["ws_bytes"], None, None)
+    if routed:
+        return lib.moe_int8_ffn_fwd(*head, a["w"], a["offsets"], a["pos"], a["y"], a["n"], a["d"], a["f"], a["e"],
+                                    a["k"], *tail)
+    return lib.int8_ffn_fwd(*head, a["y"], a["n"], a["d"], a["f"], *tail)
+
+
+@pytest.mark.parametrize("routed", [False, True])
+def test_int8_ffn_rejects_bad_arguments(lib, routed):
+    assert _ffn(lib, routed, n=0, x=None, y=None, ws=None) == 0
+    assert _ffn(lib, routed, n=-1) == 1
+    assert _ffn(lib, routed, d=0) == 1
+    assert _ffn(lib, routed, d=60) == 1
+    assert _ffn(lib, routed, f=100) == 1
+    assert _ffn(lib, routed, dt=4) == 2
+    assert _ffn(lib, routed, d=200000) == 2
+    assert _ffn(lib, routed, n=1 << 30) == 2
+    assert _ffn(lib, routed, x=None) == 1
+    assert b"null" in lib.sge_last_error()
+    assert _ffn(lib, routed, y=ctypes.c_void_p(4104)) == 1
+    assert b"aligned" in lib.sge_last_error()
+    assert _ffn(lib, routed, ws=ctypes.c_void_p(4096 + 64)) == 1
+    assert _ffn(lib, routed, ws_bytes=256) == 1
+    assert b"workspace" in lib.sge_last_error()
+    if routed:
+        assert _ffn(lib, routed, e=0) == 1
+        assert _ffn(lib, routed, k=5) == 1
+        assert _ffn(lib, routed, e=257) == 2
+        assert _ffn(lib, routed, e=64, k=17) == 2
+        assert _ffn(lib, routed, w=None) == 1
+        assert _ffn(lib, routed, offsets=None) == 1
+        assert _ffn(lib, routed, pos=ctypes.c_void_p(4100)) == 1
+    need = lib.int8_ffn_workspace_bytes(10, 64, 128, 4, 2, sge.SGE_BF16)
+    assert need > 0 and need % 256 == 0
+    assert lib.int8_ffn_workspace_bytes(10, 60, 128, 4, 2, sge.SGE_BF16) == 0

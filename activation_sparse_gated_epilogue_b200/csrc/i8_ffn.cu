@@ -200,8 +200,8 @@ struct FfnPlan {
 
 using GateUpPair = I8Shape<128, 2, 2, 1, true>;
 using GateUpOne = I8Shape<128, 2, 2, 1, false>;
-using DownPair = I8Shape<256, 1, 2, 2, true, true>;
-using DownOne = I8Shape<128, 1, 4, 1, false, true>;
+using DownPair = I8Shape<128, 1, 4, 2, true, true>;
+using DownOne = I8Shape<128, 1, 4, 2, false, true>;
 
 static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype, bool routed) {
   FfnPlan p = {};

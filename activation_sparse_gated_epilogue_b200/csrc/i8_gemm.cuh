@@ -33,12 +33,21 @@ template <int BN_, int NB_, int NACC_, int HALVES_, bool PAIR_, bool PER_BLOCK_ 
 struct I8Shape {
   static constexpr int BN = BN_, NB = NB_, NACC = NACC_, HALVES = HALVES_;
   static constexpr bool PAIR = PAIR_, PER_BLOCK = PER_BLOCK_;
-  static constexpr int THREADS = 64 + 128 * HALVES;
+  // warps before the epilogue's: 2, or a warpgroup of 4 where registers move
+  // from it to the epilogue (setmaxnreg works on whole warpgroups)
+  static constexpr bool MOVE_REGS = false;
+  static constexpr int FIRST_EPI = MOVE_REGS ? 4 : 2;
+  static constexpr int THREADS = 32 * FIRST_EPI + 128 * HALVES;
   static constexpr int BM = PAIR ? 2 * kBM : kBM;
-  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of each B tile this CTA loads
+  // B rows of one load.  NB = 2: two matrices' tiles of BN rows side by side
+  // are one operand of 2 BN rows (one MMA with N = 256 reads A once; two with
+  // N = 128 took 1.3 times as long); of a pair each CTA loads one matrix's.
+  static constexpr int B_ROWS = PAIR ? NB * BN / 2 : BN;
+  static constexpr int B_LOADS = PAIR ? 1 : NB;
+  static constexpr int MMA_N = NB * BN;
   static constexpr int A_BYTES = kBM * kI8BK;
   static constexpr int B_BYTES = B_ROWS * kI8BK;
-  static constexpr int STAGE_BYTES = A_BYTES + NB * B_BYTES;
+  static constexpr int STAGE_BYTES = A_BYTES + B_LOADS * B_BYTES;
   static constexpr int STAGES = (196 * 1024) / STAGE_BYTES > 8 ? 8 : (196 * 1024) / STAGE_BYTES;
   static constexpr int ACC_COLS = BN * NB;
   static constexpr int USED_COLS = NACC * ACC_COLS;
@@ -46,7 +55,7 @@ struct I8Shape {
                                    : USED_COLS <= 256 ? 256 : 512;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 /*align slack*/ + 512 /*barriers*/;
   static_assert(USED_COLS <= 512, "TMEM columns");
-  static_assert(BN % (PAIR ? 32 : 16) == 0 && BN <= 256, "UMMA N");
+  static_assert(MMA_N % (PAIR ? 32 : 16) == 0 && MMA_N <= 256, "UMMA N");
   static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "1024-byte aligned sub-tiles");
   static_assert(HALVES == 1 || NB == 1, "column halves need one accumulator");
   static_assert(!PER_BLOCK || NB == 1, "per-block scales: one accumulator");
@@ -171,6 +180,40 @@ SGE_DEV void i8_commit(uint64_t* bar) {
   else umma_commit(bar);
 }
 
+// Two floats in a 64-bit register, and the instructions on such pairs.
+constexpr uint32_t kFloatBits = 0x4b400000u;                // 1.5 * 2^23
+constexpr uint64_t kMinusFloat2 = 0xcb400000cb400000ull;    // minus it, twice
+SGE_DEV uint64_t pack2_bits(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+SGE_DEV uint64_t pack2(float lo, float hi) { return pack2_bits(__float_as_uint(lo), __float_as_uint(hi)); }
+SGE_DEV void unpack2(uint64_t v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+SGE_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SGE_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Arrive on a barrier of another CTA of the cluster.  CTA scope: what it
+// orders is this warp's tensor-memory reads, done before the tcgen05 fence in
+// front of it; cluster scope would also wait for the warp's global stores and
+// loads in flight, once per accumulator.
+SGE_DEV void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // What an epilogue call gets: the accumulator's TMEM address (this warp's
 // lanes, its first column), this thread's row and its tile.
 struct I8Out {
@@ -273,26 +316,28 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
   const int k_blocks = (p.k + kI8BK - 1) / kI8BK;
   const int num_tiles = sched.tiles(p);
 
-  if (warp == 0) {
-    // ------------------------------------------------------ TMA producer
-    if (lane == 0) {
+  // MOVE_REGS: 384 threads start with 168 registers each (64,512 in all); 56 for
+  // the first warpgroup and 224 for the two epilogue warpgroups are as many
+  if (warp < Shape::FIRST_EPI) {
+    if constexpr (Shape::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------- TMA producer
       int s = 0;
       uint32_t ph = 0, armed = 0, armed_par = 0;
       const uint32_t bytes =
-          PAIR ? 2 * Shape::STAGE_BYTES : a_box_rows(p.rows) * kI8BK + NB * Shape::B_BYTES;
+          PAIR ? 2 * Shape::STAGE_BYTES : a_box_rows(p.rows) * kI8BK + Shape::B_LOADS * Shape::B_BYTES;
       for (int t = worker; t < num_tiles && !*abort_flag; t += n_workers) {
         const I8Tile tc = sched.tile(p, t, k_blocks);
         const int a_row = tc.row0 + static_cast<int>(rank) * kBM;
-        const int b_row = tc.group * p.n + tc.col0 + static_cast<int>(rank) * Shape::B_ROWS;
+        const int b_row = tc.group * p.n + tc.col0 + (NB == 1 ? static_cast<int>(rank) * Shape::B_ROWS : 0);
         for (int kb = tc.kb0; kb < tc.kb1; ++kb) {
           if (!wait_or_abort(&empty[s], ph ^ 1, abort_flag, diag)) break;
           uint8_t* sa = smem + s * Shape::STAGE_BYTES;
           if (leader) mbar_arrive_expect_tx(&full[s], bytes);
           if constexpr (PAIR) {
             tma_load_2d_pair(sa, &map_a, &full[s], kb * kI8BK, a_row);
-            tma_load_2d_pair(sa + Shape::A_BYTES, &map_b0, &full[s], kb * kI8BK, b_row);
-            if (NB == 2)
-              tma_load_2d_pair(sa + Shape::A_BYTES + Shape::B_BYTES, &map_b1, &full[s], kb * kI8BK, b_row);
+            tma_load_2d_pair(sa + Shape::A_BYTES, NB == 1 || leader ? &map_b0 : &map_b1, &full[s], kb * kI8BK,
+                             b_row);
           } else {
             tma_load_2d(sa, &map_a, &full[s], kb * kI8BK, a_row);
             tma_load_2d(sa + Shape::A_BYTES, &map_b0, &full[s], kb * kI8BK, b_row);
@@ -311,11 +356,16 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
       if (leader)
         for (int t = 0; t < STAGES; ++t)
           if (armed & (1u << t)) mbar_wait(&full[t], (armed_par >> t) & 1, diag);
-    }
-  } else if (warp == 1) {
-    // -------------------------------------------------------- MMA issuer
-    if (leader && lane == 0) {
-      constexpr uint32_t idesc = umma_idesc_i8(Shape::BM, BN);
+    } else if (warp == 1 && leader) {
+      // ------------------------------------------------------ MMA issuer
+      // The whole warp walks the loop and one elected thread issues: with
+      // uniform control flow around them the instructions go out several
+      // times faster than from a single diverged lane (one lane took about
+      // 700 cycles for the four MMAs of a stage, whatever their N).
+      constexpr uint32_t idesc = umma_idesc_i8(Shape::BM, Shape::MMA_N);
+      const uint64_t adesc0 = umma_desc_sw128(smem_u32(smem));
+      const uint64_t bdesc0 = umma_desc_sw128(smem_u32(smem) + Shape::A_BYTES);
+      const bool elected = elect_one_sync();
       int s = 0, acc = 0;
       uint32_t ph = 0, acc_ph = 0;
       bool ok = true;
@@ -324,55 +374,52 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
         for (int kb = tc.kb0; kb < tc.kb1; ++kb) {
           const bool fresh = PER_BLOCK || kb == tc.kb0;
           if (fresh) {
-            ok = wait_or_abort(&tmem_empty[acc], acc_ph ^ 1, abort_flag, diag);
+            ok = __all_sync(0xffffffffu, wait_or_abort(&tmem_empty[acc], acc_ph ^ 1, abort_flag, diag));
             if (!ok) break;
           }
-          ok = wait_or_abort(&full[s], ph, abort_flag, diag);
+          ok = __all_sync(0xffffffffu, wait_or_abort(&full[s], ph, abort_flag, diag));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + acc * Shape::ACC_COLS;
-          const uint32_t sa = smem_u32(smem + s * Shape::STAGE_BYTES);
+          if (elected) {
+            const uint32_t d_tmem = tmem_base + acc * Shape::ACC_COLS;
+            const uint64_t at = static_cast<uint64_t>(s * (Shape::STAGE_BYTES >> 4));
 #pragma unroll
-          for (int k = 0; k < kI8BK / 32; ++k) {
-            const uint64_t adesc = umma_desc_sw128(sa + k * 32);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              const uint64_t bdesc = umma_desc_sw128(sa + Shape::A_BYTES + b * Shape::B_BYTES + k * 32);
-              umma_i8<PAIR>(d_tmem + b * BN, adesc, bdesc, idesc, (!fresh || k != 0) ? 1u : 0u);
-            }
+            for (int k = 0; k < kI8BK / 32; ++k)
+              umma_i8<PAIR>(d_tmem, adesc0 + at + 2 * k, bdesc0 + at + 2 * k, idesc, (!fresh || k != 0) ? 1u : 0u);
+            i8_commit<PAIR>(&empty[s]);
+            if (!PER_BLOCK && kb == tc.kb1 - 1) i8_commit<PAIR>(&tmem_full[acc]);
           }
-          i8_commit<PAIR>(&empty[s]);
+          __syncwarp();
           if (++s == STAGES) {
             s = 0;
             ph ^= 1;
           }
-          if (PER_BLOCK || kb == tc.kb1 - 1) {
-            i8_commit<PAIR>(&tmem_full[acc]);
-            if (++acc == NACC) {
-              acc = 0;
-              acc_ph ^= 1;
-            }
+          if ((PER_BLOCK || kb == tc.kb1 - 1) && ++acc == NACC) {
+            acc = 0;
+            acc_ph ^= 1;
           }
         }
       }
-      i8_commit<PAIR>(drain);  // completes once every MMA issued above has
+      if (elected) i8_commit<PAIR>(drain);  // completes once every MMA issued above has
+      __syncwarp();
     }
-    if (lane == 0) mbar_wait(drain, 0, diag);
+    if (warp == 1 && lane == 0) mbar_wait(drain, 0, diag);
     __syncwarp();
   } else {
     // --------------------------------------------------------- epilogue
+    if constexpr (Shape::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int quarter = warp & 3;      // TMEM lanes this warp may access
-    const int half = (warp - 2) >> 2;  // column half (HALVES = 2)
+    const int half = (warp - Shape::FIRST_EPI) >> 2;  // column half (HALVES = 2)
     constexpr int COLS = BN / Shape::HALVES;
     const uint32_t lane_base = tmem_base + half * COLS + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t release0 = PAIR ? mapa_shared(smem_u32(&tmem_empty[0]), 0) : 0;
-    int acc = 0;
-    uint32_t acc_ph = 0;
+    int acc = 0, s_done = 0;  // s_done: the stage of the block at hand (PER_BLOCK)
+    uint32_t acc_ph = 0, s_ph = 0;
     const auto release = [&] {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (PAIR) mbar_arrive_cluster(release0 + acc * 8);
+        if constexpr (PAIR) mbar_arrive_remote(release0 + acc * 8);
         else mbar_arrive(&tmem_empty[acc]);
       }
       if (++acc == NACC) {
@@ -391,28 +438,56 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
       o.group = tc.group;
       o.split = tc.split;
       if constexpr (PER_BLOCK) {
-        float sum[COLS];
+        // pairs of columns: adds and multiply-adds of two floats per instruction
+        uint64_t sum2[COLS / 2];
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) sum[j] = 0.0f;
-        float scale = epi.block_scale(o, tc.kb0);
-        for (int kb = tc.kb0; kb < tc.kb1; ++kb) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(&tmem_full[acc], acc_ph, abort_flag, diag));
-          if (!ok) break;
-          tc_fence_after();
-          const float s = scale;
-          if (kb + 1 < tc.kb1) scale = epi.block_scale(o, kb + 1);  // in flight during this block
+        for (int j = 0; j < COLS / 2; ++j) sum2[j] = 0;
+        // four blocks' scales are loaded while the four before are added: a
+        // block takes a few hundred cycles, a load from L2 longer
+        constexpr int AHEAD = 4;
+        float next[AHEAD];
 #pragma unroll
-          for (int ch = 0; ch < COLS / 32; ++ch) {
-            uint32_t r[32];
-            tmem_ld32(lane_base + acc * Shape::ACC_COLS + ch * 32, r);
-            tmem_ld_wait();
+        for (int i = 0; i < AHEAD; ++i) next[i] = tc.kb0 + i < tc.kb1 ? epi.block_scale(o, tc.kb0 + i) : 0.0f;
+        for (int kb4 = tc.kb0; ok && kb4 < tc.kb1; kb4 += AHEAD) {
+          float scale[AHEAD];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              sum[ch * 32 + j] = fmaf(__int2float_rn(static_cast<int>(r[j])), s, sum[ch * 32 + j]);
+          for (int i = 0; i < AHEAD; ++i) {
+            scale[i] = next[i];
+            const int kb = kb4 + AHEAD + i;
+            next[i] = kb < tc.kb1 ? epi.block_scale(o, kb) : 0.0f;
           }
-          release();
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            if (kb4 + i >= tc.kb1) break;
+            // the commit that frees the block's stage also says that its sums are there
+            ok = __all_sync(0xffffffffu, wait_or_abort(&empty[s_done], s_ph, abort_flag, diag));
+            if (!ok) break;
+            if (++s_done == STAGES) {
+              s_done = 0;
+              s_ph ^= 1;
+            }
+            tc_fence_after();
+            uint32_t r[COLS];
+#pragma unroll
+            for (int ch = 0; ch < COLS / 32; ++ch)
+              tmem_ld32(lane_base + acc * Shape::ACC_COLS + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(r + ch * 32));
+            tmem_ld_wait();
+            release();  // the block's sums are in registers: the MMA may write the next over them
+            const uint64_t s2 = pack2(scale[i], scale[i]);
+            // |sum of a block| <= 128 * 127 * 127 < 2^22: added to the bits of 1.5 * 2^23 it gives
+            // the float 1.5 * 2^23 + sum, from which the constant comes off exactly
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j)
+              sum2[j] = fma2(add2(pack2_bits(r[2 * j] + kFloatBits, r[2 * j + 1] + kFloatBits), kMinusFloat2), s2,
+                             sum2[j]);
+          }
         }
-        if (ok) epi.template store<COLS>(o, sum, p.n);
+        if (ok) {
+          float sum[COLS];
+#pragma unroll
+          for (int j = 0; j < COLS / 2; ++j) unpack2(sum2[j], sum[2 * j], sum[2 * j + 1]);
+          epi.template store<COLS>(o, sum, p.n);
+        }
       } else {
         ok = __all_sync(0xffffffffu, wait_or_abort(&tmem_full[acc], acc_ph, abort_flag, diag));
         if (!ok) break;

@@ -470,18 +470,47 @@ def hybrid_ffn_bwd(x: torch.Tensor, dy: torch.Tensor, hy: Hybrid, wg_t: torch.Te
 # ------------------------------------------------- 8-bit integer products
 
 
-def _launch(name: str, dev: torch.device, stream, *args) -> None:
-    """Call `name` with the stream appended, on the tensors' device."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call(name, *args, _stream(dev, stream))
-    _call(name, *args, _stream(dev, stream))
+# A decode step makes many small calls, so the checks below read each property
+# of a tensor once and form no message unless one fails.
 
 
-def _same_device(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, x on {dev}")
+def _launch(name: str, index: int, stream, *args) -> None:
+    """Call `name` with the stream appended, on CUDA device `index`."""
+    lib = _lib or library()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            rc = getattr(lib, name)(*args, _raw_stream(index, stream))
+    else:
+        rc = getattr(lib, name)(*args, _raw_stream(index, stream))
+    if rc != 0:
+        raise LibraryError(name, rc, lib.sge_last_error().decode())
+
+
+def _raw_stream(index: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    return index
+
+
+def _operand(t: torch.Tensor, name: str, index: int, dtype, shape) -> int:
+    """The address of a contiguous tensor of this dtype and shape on device `index`."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        _check(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, other operands on cuda:{index}")
+    return t.data_ptr()
+
+
+def _scratch(t: torch.Tensor, index: int) -> int:
+    return _operand(t, "workspace", index, torch.uint8, (t.numel(),))
+
+
+def _diag_ptr(diag: Optional[torch.Tensor], index: int) -> Optional[int]:
+    return None if diag is None else _operand(diag, "diag", index, torch.int32, (4,))
 
 
 def _used_on(stream, *tensors) -> None:
@@ -510,33 +539,36 @@ class Int8Rows:
     def rows(self) -> int:
         return self.q.shape[0]
 
-    def _check(self, name: str, rows: Optional[int] = None, cols: Optional[int] = None) -> None:
-        q = _check(self.q, f"{name}.q", torch.int8)
+    def _operands(self, name: str, index: int, rows: Optional[int] = None, cols: Optional[int] = None):
+        """(address of q, pitch, address of scale), checked."""
+        q = self.q
         if q.dim() != 2 or q.shape[1] % 16 or not 1 <= self.cols <= q.shape[1]:
             raise ValueError(f"{name}.q must be [rows][pitch], pitch a multiple of 16, at least cols")
-        _check(self.scale, f"{name}.scale", torch.float32, (q.shape[0],))
-        if rows is not None and q.shape[0] != rows:
-            raise ValueError(f"{name} must have {rows} rows, got {q.shape[0]}")
+        n, pitch = q.shape
+        if rows is not None and n != rows:
+            raise ValueError(f"{name} must have {rows} rows, got {n}")
         if cols is not None and self.cols != cols:
             raise ValueError(f"{name} must have {cols} columns, got {self.cols}")
+        return (_operand(q, f"{name}.q", index, torch.int8, (n, pitch)), pitch,
+                _operand(self.scale, f"{name}.scale", index, torch.float32, (n,)))
 
 
 def int8_quant_rows(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None) -> Int8Rows:
     """The rows of a bf16 or fp32 matrix as 8-bit integers with a scale each
     (activations per token; weights per output channel, done once when they
     are loaded).  x may be a row-strided view."""
+    index = _device_of(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     n, d = x.shape
-    ldx = _check_rows(x, "x", x.dtype, (n, d))
+    if d > 1 and x.stride(1) != 1:
+        raise ValueError("x must have contiguous rows")
+    ldx = x.stride(0) if n > 1 else d
     if out is None:
         out = Int8Rows.empty(n, d, x.device)
         _used_on(stream, out.q, out.scale)
-    else:
-        out._check("out", n, d)
-        _same_device(x.device, out=out.q, scale=out.scale)
-    _launch("int8_quant_rows", x.device, stream, _ptr(x), ldx, n, d, _dtype_code(x), _ptr(out.q),
-            out.q.shape[1], _ptr(out.scale))
+    q, ldq, scale = out._operands("out", index, n, d)
+    _launch("int8_quant_rows", index, stream, x.data_ptr(), ldx, n, d, _dtype_code(x), q, ldq, scale)
     return out
 
 
@@ -545,19 +577,16 @@ def int8_linear(xq: Int8Rows, wq: Int8Rows, dtype: torch.dtype = torch.bfloat16,
                 stream=None) -> torch.Tensor:
     """y[n][m] = (sum over k of xq[n][k] * wq[m][k]) * xq.scale[n] * wq.scale[m]
     with exact integer sums, in bf16 or fp32."""
-    xq._check("xq")
-    wq._check("wq", cols=xq.cols)
-    n, m, dev = xq.rows, wq.rows, xq.q.device
+    index = _device_of(xq.q, "xq")
+    k = xq.cols
+    x, ldx, sx = xq._operands("xq", index)
+    w, ldw, sw = wq._operands("wq", index, cols=k)
+    n, m = xq.q.shape[0], wq.q.shape[0]
     if y is None:
-        y = torch.empty((n, m), dtype=dtype, device=dev)
+        y = torch.empty((n, m), dtype=dtype, device=xq.q.device)
         _used_on(stream, y)
-    else:
-        _check(y, "y", dtype, (n, m))
-    if diag is not None:
-        _check(diag, "diag", torch.int32, (4,))
-    _same_device(dev, sx=xq.scale, wq=wq.q, sw=wq.scale, y=y, diag=diag)
-    _launch("int8_linear", dev, stream, _ptr(xq.q), xq.q.shape[1], _ptr(xq.scale), _ptr(wq.q),
-            wq.q.shape[1], _ptr(wq.scale), _ptr(y), n, m, xq.cols, _dtype_code(y), _ptr(diag))
+    _launch("int8_linear", index, stream, x, ldx, sx, w, ldw, sw, _operand(y, "y", index, dtype, (n, m)), n, m, k,
+            _dtype_code(y), _diag_ptr(diag, index))
     return y
 
 
@@ -565,23 +594,18 @@ def twell_gate_pack_int8(xq: Int8Rows, wg_q: Int8Rows, tile: int, cap: int, out:
                          diag: Optional[torch.Tensor] = None, stream=None) -> TwELL:
     """twell_gate_pack with the gate projection in 8-bit integers: TwELL
     (bf16 values) of ReLU of int8_linear's product."""
-    xq._check("xq")
-    wg_q._check("wg_q", cols=xq.cols)
-    n, f, dev = xq.rows, wg_q.rows, xq.q.device
+    index = _device_of(xq.q, "xq")
+    k = xq.cols
+    x, ldx, sx = xq._operands("xq", index)
+    w, ldw, sw = wg_q._operands("wg_q", index, cols=k)
+    n, f = xq.q.shape[0], wg_q.q.shape[0]
     if out is None:
-        out = TwELL.empty(n, f, tile, cap, torch.bfloat16, dev)
+        out = TwELL.empty(n, f, tile, cap, torch.bfloat16, xq.q.device)
         _used_on(stream, out.count, out.idx, out.val)
-    else:
-        _check(out.count, "count", torch.uint8, (n, f // tile))
-        _check(out.idx, "idx", torch.uint8, (n, f // tile, cap))
-        _check(out.val, "val", torch.bfloat16, (n, f // tile, cap))
-    if diag is not None:
-        _check(diag, "diag", torch.int32, (4,))
-    _same_device(dev, sx=xq.scale, wg_q=wg_q.q, sw=wg_q.scale, count=out.count, idx=out.idx, val=out.val,
-                 diag=diag)
-    _launch("twell_gate_pack_int8", dev, stream, _ptr(xq.q), xq.q.shape[1], _ptr(xq.scale), _ptr(wg_q.q),
-            wg_q.q.shape[1], _ptr(wg_q.scale), n, xq.cols, f, tile, cap, _ptr(out.count), _ptr(out.idx),
-            _ptr(out.val), _ptr(diag))
+    _launch("twell_gate_pack_int8", index, stream, x, ldx, sx, w, ldw, sw, n, k, f, tile, cap,
+            _operand(out.count, "count", index, torch.uint8, (n, f // tile)),
+            _operand(out.idx, "idx", index, torch.uint8, (n, f // tile, cap)),
+            _operand(out.val, "val", index, torch.bfloat16, (n, f // tile, cap)), _diag_ptr(diag, index))
     return out
 
 
@@ -610,15 +634,6 @@ class MoeRoute:
         return MoeRoute(i(n_tokens, top_k), f(n_tokens, top_k), i(n_experts), i(n_experts + 1),
                         i(n_tokens, top_k), i(n_tokens * top_k), f(1), i(1))
 
-    def _check(self, n: int, e: int, k: int, dev) -> None:
-        for name, dt, shape in (("ids", torch.int32, (n, k)), ("w", torch.float32, (n, k)),
-                                ("counts", torch.int32, (e,)), ("offsets", torch.int32, (e + 1,)),
-                                ("pos", torch.int32, (n, k)), ("order", torch.int32, (n * k,)),
-                                ("loss", torch.float32, (1,)), ("n_live", torch.int32, (1,))):
-            t = _check(getattr(self, name), name, dt, shape)
-            if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, the logits on {dev}")
-
 
 def moe_route_workspace(n_tokens: int, n_experts: int, top_k: int, device) -> torch.Tensor:
     """Scratch for moe_route_fwd (each block's counts and probability sums)."""
@@ -626,16 +641,17 @@ def moe_route_workspace(n_tokens: int, n_experts: int, top_k: int, device) -> to
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
-def _check_logits(logits: torch.Tensor, mask: Optional[torch.Tensor]):
-    _check(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [tokens][experts]")
-    if mask is not None:
-        if mask.dtype not in (torch.uint8, torch.bool):
-            raise ValueError(f"mask must be uint8 or bool, got {mask.dtype}")
-        _check(mask, "mask", None, (logits.shape[0],))
-        _same_device(logits.device, mask=mask)
-    return logits.shape
+def _logits_operands(logits: torch.Tensor, mask: Optional[torch.Tensor]):
+    """(device, tokens, experts, address of the logits, of the mask), checked."""
+    index = _device_of(logits, "logits")
+    if logits.dim() != 2 or not logits.is_contiguous():
+        raise ValueError("logits must be [tokens][experts], contiguous")
+    n, e = logits.shape
+    if mask is None:
+        return index, n, e, logits.data_ptr(), None
+    if mask.dtype not in (torch.uint8, torch.bool):
+        raise ValueError(f"mask must be uint8 or bool, got {mask.dtype}")
+    return index, n, e, logits.data_ptr(), _operand(mask, "mask", index, mask.dtype, (n,))
 
 
 def moe_route_fwd(logits: torch.Tensor, top_k: int, renorm: bool = True, mask: Optional[torch.Tensor] = None,
@@ -643,23 +659,22 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, renorm: bool = True, mask: O
                   stream=None) -> MoeRoute:
     """Top-k experts and weights of each token, assignments per expert, their
     expert order, and the balance loss.  ``mask`` [N]: 0 for padding tokens."""
-    n, e = _check_logits(logits, mask)
-    dev = logits.device
+    index, n, e, x, m = _logits_operands(logits, mask)
     if out is None:
-        out = MoeRoute.empty(n, e, max(top_k, 0), dev)
+        out = MoeRoute.empty(n, e, max(top_k, 0), logits.device)
         _used_on(stream, out.ids, out.w, out.counts, out.offsets, out.pos, out.order, out.loss, out.n_live)
-    else:
-        out._check(n, e, top_k, dev)
     out.renorm = bool(renorm)
     if workspace is None:
-        workspace = moe_route_workspace(n, e, top_k, dev)
+        workspace = moe_route_workspace(n, e, top_k, logits.device)
         _used_on(stream, workspace)
-    else:
-        _check(workspace, "workspace", torch.uint8)
-        _same_device(dev, workspace=workspace)
-    _launch("moe_route_fwd", dev, stream, _ptr(logits), _ptr(mask), n, e, top_k, int(out.renorm),
-            _dtype_code(logits), _ptr(out.ids), _ptr(out.w), _ptr(out.counts), _ptr(out.offsets), _ptr(out.pos),
-            _ptr(out.order), _ptr(out.loss), _ptr(out.n_live), _ptr(workspace), workspace.numel())
+    i32, f32, nk = torch.int32, torch.float32, (n, top_k)
+    _launch("moe_route_fwd", index, stream, x, m, n, e, top_k, int(out.renorm), _dtype_code(logits),
+            _operand(out.ids, "ids", index, i32, nk), _operand(out.w, "w", index, f32, nk),
+            _operand(out.counts, "counts", index, i32, (e,)),
+            _operand(out.offsets, "offsets", index, i32, (e + 1,)),
+            _operand(out.pos, "pos", index, i32, nk), _operand(out.order, "order", index, i32, (n * top_k,)),
+            _operand(out.loss, "loss", index, f32, (1,)), _operand(out.n_live, "n_live", index, i32, (1,)),
+            _scratch(workspace, index), workspace.numel())
     return out
 
 
@@ -668,23 +683,20 @@ def moe_route_bwd(logits: torch.Tensor, route: MoeRoute, dloss: Optional[torch.T
                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dlogits from the gradients of the balance loss (fp32 [1]) and of the
     weights (fp32 [N][k]); logits and mask as in the forward that gave route."""
-    n, e = _check_logits(logits, mask)
-    dev = logits.device
+    index, n, e, x, m = _logits_operands(logits, mask)
     k = route.ids.shape[1]
-    route._check(n, e, k, dev)
-    if dloss is not None:
-        _check(dloss, "dloss", torch.float32, (1,))
-    if dw is not None:
-        _check(dw, "dw", torch.float32, (n, k))
     if out is None:
         out = torch.empty_like(logits)
         _used_on(stream, out)
-    else:
-        _check(out, "out", logits.dtype, (n, e))
-    _same_device(dev, dloss=dloss, dw=dw, out=out)
-    _launch("moe_route_bwd", dev, stream, _ptr(logits), _ptr(mask), n, e, k, int(route.renorm),
-            _dtype_code(logits), _ptr(route.ids), _ptr(route.w), _ptr(route.counts), _ptr(route.offsets),
-            _ptr(route.n_live), _ptr(dloss), _ptr(dw), _ptr(out))
+    i32, f32 = torch.int32, torch.float32
+    _launch("moe_route_bwd", index, stream, x, m, n, e, k, int(route.renorm), _dtype_code(logits),
+            _operand(route.ids, "ids", index, i32, (n, k)), _operand(route.w, "w", index, f32, (n, k)),
+            _operand(route.counts, "counts", index, i32, (e,)),
+            _operand(route.offsets, "offsets", index, i32, (e + 1,)),
+            _operand(route.n_live, "n_live", index, i32, (1,)),
+            None if dloss is None else _operand(dloss, "dloss", index, f32, (1,)),
+            None if dw is None else _operand(dw, "dw", index, f32, (n, k)),
+            _operand(out, "out", index, logits.dtype, (n, e)))
     return out
 
 
@@ -698,33 +710,28 @@ def int8_ffn_workspace(n_tokens: int, d_model: int, d_ff: int, n_experts: int, t
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
-def _ffn_args(x, wg_q, wu_q, wd_t_q, e, k, y, workspace, diag, stream):
-    """Checked operands of the two calls: (n, d, f, y, workspace)."""
-    _check(x, "x")
+def _ffn_operands(x, index, wg_q, wu_q, wd_t_q, e, k, y, workspace, stream):
+    """Checked operands of the two calls: (n, d, f, addresses of the weights
+    and scales, y, workspace)."""
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be [tokens][d_model], contiguous")
     n, d = x.shape
-    dev = x.device
     if wg_q.rows % e:
         raise ValueError(f"wg_q must have a multiple of {e} rows, got {wg_q.rows}")
     f = wg_q.rows // e
+    weights = []
     for name, m, rows, cols in (("wg_q", wg_q, e * f, d), ("wu_q", wu_q, e * f, d), ("wd_t_q", wd_t_q, e * d, f)):
-        m._check(name, rows, cols)
-        if m.q.shape[1] != (cols + 15) // 16 * 16:
-            raise ValueError(f"{name}.q must have rows of {(cols + 15) // 16 * 16} bytes, got {m.q.shape[1]}")
+        q, pitch, scale = m._operands(name, index, rows, cols)
+        if pitch != (cols + 15) // 16 * 16:
+            raise ValueError(f"{name}.q must have rows of {(cols + 15) // 16 * 16} bytes, got {pitch}")
+        weights += (q, scale)
     if y is None:
         y = torch.empty_like(x)
         _used_on(stream, y)
-    else:
-        _check(y, "y", x.dtype, (n, d))
     if workspace is None:
-        workspace = int8_ffn_workspace(n, d, f, e, k, x.dtype, dev)
+        workspace = int8_ffn_workspace(n, d, f, e, k, x.dtype, x.device)
         _used_on(stream, workspace)
-    else:
-        _check(workspace, "workspace", torch.uint8)
-    if diag is not None:
-        _check(diag, "diag", torch.int32, (4,))
-    _same_device(dev, wg_q=wg_q.q, sg=wg_q.scale, wu_q=wu_q.q, su=wu_q.scale, wd_t_q=wd_t_q.q, sd=wd_t_q.scale,
-                 y=y, workspace=workspace, diag=diag)
-    return n, d, f, y, workspace
+    return n, d, f, weights, y, workspace
 
 
 def int8_ffn_fwd(x: torch.Tensor, wg_q: Int8Rows, wu_q: Int8Rows, wd_t_q: Int8Rows,
@@ -732,10 +739,10 @@ def int8_ffn_fwd(x: torch.Tensor, wg_q: Int8Rows, wu_q: Int8Rows, wd_t_q: Int8Ro
                  diag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gated feed-forward block on 8-bit weights.  ``wd_t_q`` is
     int8_quant_rows of W_down transposed, [d][F]."""
-    n, d, f, y, workspace = _ffn_args(x, wg_q, wu_q, wd_t_q, 1, 1, y, workspace, diag, stream)
-    _launch("int8_ffn_fwd", x.device, stream, _ptr(x), _ptr(wg_q.q), _ptr(wg_q.scale), _ptr(wu_q.q),
-            _ptr(wu_q.scale), _ptr(wd_t_q.q), _ptr(wd_t_q.scale), _ptr(y), n, d, f, _dtype_code(x),
-            _ptr(workspace), workspace.numel(), _ptr(diag))
+    index = _device_of(x, "x")
+    n, d, f, weights, y, workspace = _ffn_operands(x, index, wg_q, wu_q, wd_t_q, 1, 1, y, workspace, stream)
+    _launch("int8_ffn_fwd", index, stream, x.data_ptr(), *weights, _operand(y, "y", index, x.dtype, (n, d)), n, d, f,
+            _dtype_code(x), _scratch(workspace, index), workspace.numel(), _diag_ptr(diag, index))
     return y
 
 
@@ -746,13 +753,14 @@ def moe_int8_ffn_fwd(x: torch.Tensor, wg_q: Int8Rows, wu_q: Int8Rows, wd_t_q: In
     """The experts' blocks on 8-bit weights (expert by expert in the rows of
     wg_q, wu_q and wd_t_q), each token's summed with its weights; w, offsets
     and pos are moe_route_fwd's."""
+    index = _device_of(x, "x")
     e, k = offsets.shape[0] - 1, w.shape[1]
-    n, d, f, y, workspace = _ffn_args(x, wg_q, wu_q, wd_t_q, e, k, y, workspace, diag, stream)
-    _check(w, "w", torch.float32, (n, k))
-    _check(offsets, "offsets", torch.int32, (e + 1,))
-    _check(pos, "pos", torch.int32, (n, k))
-    _same_device(x.device, w=w, offsets=offsets, pos=pos)
-    _launch("moe_int8_ffn_fwd", x.device, stream, _ptr(x), _ptr(wg_q.q), _ptr(wg_q.scale), _ptr(wu_q.q),
-            _ptr(wu_q.scale), _ptr(wd_t_q.q), _ptr(wd_t_q.scale), _ptr(w), _ptr(offsets), _ptr(pos), _ptr(y), n, d,
-            f, e, k, _dtype_code(x), _ptr(workspace), workspace.numel(), _ptr(diag))
+    if e < 1:
+        raise ValueError("offsets must be [experts + 1]")
+    n, d, f, weights, y, workspace = _ffn_operands(x, index, wg_q, wu_q, wd_t_q, e, k, y, workspace, stream)
+    _launch("moe_int8_ffn_fwd", index, stream, x.data_ptr(), *weights,
+            _operand(w, "w", index, torch.float32, (n, k)),
+            _operand(offsets, "offsets", index, torch.int32, (e + 1,)),
+            _operand(pos, "pos", index, torch.int32, (n, k)), _operand(y, "y", index, x.dtype, (n, d)), n, d, f, e, k,
+            _dtype_code(x), _scratch(workspace, index), workspace.numel(), _diag_ptr(diag, index))
     return y

@@ -127,17 +127,24 @@ struct EpiI8Down {
 
   template <int COLS>
   __device__ __forceinline__ void store(const I8Out& o, const float (&sum)[COLS], int n) const {
-    if (!o.row_ok) return;
-    const float* cd = sd + static_cast<int64_t>(o.group) * n + o.col0;
+    const float* cd = sd + static_cast<int64_t>(o.group) * n;
     T* out = z + (o.split * rows + o.row) * n + o.col0;
 #pragma unroll
-    for (int j = 0; j < COLS; j += 8) {
-      if (o.col0 + j >= n) break;  // n % 8 == 0
-      const float4 a = __ldg(reinterpret_cast<const float4*>(cd + j));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(cd + j + 4));
-      const float v[8] = {sum[j] * a.x,     sum[j + 1] * a.y, sum[j + 2] * a.z, sum[j + 3] * a.w,
-                          sum[j + 4] * b.x, sum[j + 5] * b.y, sum[j + 6] * b.z, sum[j + 7] * b.w};
-      store_cols<8>(out + j, v, 8, 8);
+    for (int c = 0; c < COLS; c += 32) {
+      // all scales of 32 columns first: one latency, not one per store (n % 8
+      // == 0: eight columns are inside or outside together)
+      float4 sc[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        sc[j] = __ldg(reinterpret_cast<const float4*>(cd + min(o.col0 + c + 4 * j, n - 4)));
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        const float4 a = sc[j / 4], b = sc[j / 4 + 1];
+        const float* f = &sum[c + j];
+        const float v[8] = {f[0] * a.x, f[1] * a.y, f[2] * a.z, f[3] * a.w,
+                            f[4] * b.x, f[5] * b.y, f[6] * b.z, f[7] * b.w};
+        if (o.row_ok && o.col0 + c + j < n) store_cols<8>(out + c + j, v, 8, 8);
+      }
     }
   }
 };
@@ -200,7 +207,7 @@ struct FfnPlan {
 
 using GateUpPair = I8Shape<128, 2, 2, 1, true>;
 using GateUpOne = I8Shape<128, 2, 2, 1, false>;
-using DownPair = I8Shape<128, 1, 4, 2, true, true>;
+using DownPair = I8Shape<256, 1, 2, 2, true, true>;
 using DownOne = I8Shape<128, 1, 4, 2, false, true>;
 
 static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype, bool routed) {

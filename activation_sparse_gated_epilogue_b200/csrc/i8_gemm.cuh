@@ -35,7 +35,7 @@ struct I8Shape {
   static constexpr bool PAIR = PAIR_, PER_BLOCK = PER_BLOCK_;
   // warps before the epilogue's: 2, or a warpgroup of 4 where registers move
   // from it to the epilogue (setmaxnreg works on whole warpgroups)
-  static constexpr bool MOVE_REGS = false;
+  static constexpr bool MOVE_REGS = PER_BLOCK && HALVES == 2 && BN / HALVES > 64;
   static constexpr int FIRST_EPI = MOVE_REGS ? 4 : 2;
   static constexpr int THREADS = 32 * FIRST_EPI + 128 * HALVES;
   static constexpr int BM = PAIR ? 2 * kBM : kBM;
@@ -178,32 +178,6 @@ template <bool PAIR>
 SGE_DEV void i8_commit(uint64_t* bar) {
   if constexpr (PAIR) umma2_commit_mc(bar, 0x3);
   else umma_commit(bar);
-}
-
-// Two floats in a 64-bit register, and the instructions on such pairs.
-constexpr uint32_t kFloatBits = 0x4b400000u;                // 1.5 * 2^23
-constexpr uint64_t kMinusFloat2 = 0xcb400000cb400000ull;    // minus it, twice
-SGE_DEV uint64_t pack2_bits(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-SGE_DEV uint64_t pack2(float lo, float hi) { return pack2_bits(__float_as_uint(lo), __float_as_uint(hi)); }
-SGE_DEV void unpack2(uint64_t v, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-SGE_DEV uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-SGE_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 // Arrive on a barrier of another CTA of the cluster.  CTA scope: what it
@@ -438,10 +412,9 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
       o.group = tc.group;
       o.split = tc.split;
       if constexpr (PER_BLOCK) {
-        // pairs of columns: adds and multiply-adds of two floats per instruction
-        uint64_t sum2[COLS / 2];
+        float sum[COLS];
 #pragma unroll
-        for (int j = 0; j < COLS / 2; ++j) sum2[j] = 0;
+        for (int j = 0; j < COLS; ++j) sum[j] = 0.0f;
         // four blocks' scales are loaded while the four before are added: a
         // block takes a few hundred cycles, a load from L2 longer
         constexpr int AHEAD = 4;
@@ -467,27 +440,21 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
               s_ph ^= 1;
             }
             tc_fence_after();
-            uint32_t r[COLS];
+            const uint32_t src = lane_base + acc * Shape::ACC_COLS;
+            uint32_t r[2][32];
+            tmem_ld32(src, r[0]);
 #pragma unroll
-            for (int ch = 0; ch < COLS / 32; ++ch)
-              tmem_ld32(lane_base + acc * Shape::ACC_COLS + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(r + ch * 32));
-            tmem_ld_wait();
-            release();  // the block's sums are in registers: the MMA may write the next over them
-            const uint64_t s2 = pack2(scale[i], scale[i]);
-            // |sum of a block| <= 128 * 127 * 127 < 2^22: added to the bits of 1.5 * 2^23 it gives
-            // the float 1.5 * 2^23 + sum, from which the constant comes off exactly
+            for (int ch = 0; ch < COLS / 32; ++ch) {
+              tmem_ld_wait();
+              if (ch + 1 < COLS / 32) tmem_ld32(src + (ch + 1) * 32, r[(ch + 1) & 1]);
+              else release();  // the block's last sums are in registers: the MMA may write over them
 #pragma unroll
-            for (int j = 0; j < COLS / 2; ++j)
-              sum2[j] = fma2(add2(pack2_bits(r[2 * j] + kFloatBits, r[2 * j + 1] + kFloatBits), kMinusFloat2), s2,
-                             sum2[j]);
+              for (int j = 0; j < 32; ++j)
+                sum[ch * 32 + j] = fmaf(__int2float_rn(static_cast<int>(r[ch & 1][j])), scale[i], sum[ch * 32 + j]);
+            }
           }
         }
-        if (ok) {
-          float sum[COLS];
-#pragma unroll
-          for (int j = 0; j < COLS / 2; ++j) unpack2(sum2[j], sum[2 * j], sum[2 * j + 1]);
-          epi.template store<COLS>(o, sum, p.n);
-        }
+        if (ok) epi.template store<COLS>(o, sum, p.n);
       } else {
         ok = __all_sync(0xffffffffu, wait_or_abort(&tmem_full[acc], acc_ph, abort_flag, diag));
         if (!ok) break;
@@ -523,7 +490,8 @@ int make_i8_maps(I8Maps* m, const I8Problem& p, const int8_t* a, int64_t lda, co
   const uint64_t b_rows = static_cast<uint64_t>(p.n) * p.groups;
   int rc = make_tmap_i8(&m->a, a, p.rows, p.k, lda, a_box);
   if (!rc) rc = make_tmap_i8(&m->b0, b0, b_rows, p.k, ldb, Shape::B_ROWS);
-  if (!rc) rc = make_tmap_i8(&m->b1, b1 ? b1 : b0, b_rows, p.k, ldb, Shape::B_ROWS);
+  if (!rc && b1) rc = make_tmap_i8(&m->b1, b1, b_rows, p.k, ldb, Shape::B_ROWS);
+  if (!b1) m->b1 = m->b0;  // not used
   return rc;
 }
 

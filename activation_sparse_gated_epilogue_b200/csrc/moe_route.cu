@@ -7,9 +7,10 @@
 //   counts_e = assignments of expert e,  f_e = counts_e / sum(counts)
 //   loss = E * sum_e f_e * mean over live tokens of p_e
 //
-// One warp per row: lane l holds the logits of experts l, l + 32, ...  The
-// k largest are found by k rounds of a warp-wide maximum over order-keeping
-// 32-bit keys, then the lowest index that has it, so ties are exact.  Each
+// One warp per row: lane l holds the logits of experts l * V .. l * V + V - 1.
+// The k largest are found by k rounds of a warp-wide maximum over order-keeping
+// 32-bit keys, of which the lowest lane (the lowest index) gives its first, so
+// ties are exact.  Each
 // block takes a contiguous range of rows, split into contiguous ranges of its
 // warps, and leaves its count and probability sum of every expert; a second
 // kernel adds these over the blocks (every block for itself: at most
@@ -59,68 +60,197 @@ SGE_DEV float warp_sum(float v) {
   return v;
 }
 
-// A row's logits as floats; experts past the last: -inf.
-template <class T, int V>
+// V consecutive values of a row from expert lane * V on, as floats; experts past
+// the last: -inf.  VEC: E is a multiple of V, so that a lane's values are all
+// there or all past the end, and aligned.
+template <class T, int V, bool VEC>
 SGE_DEV void load_logits(const T* row, int experts, int lane, float (&l)[V]) {
+  const int e = lane * V;
+  if constexpr (VEC) {
+    constexpr int BYTES = V * static_cast<int>(sizeof(T));
+    constexpr int UNIT = BYTES >= 16 ? 16 : BYTES;  // bytes of one load
+    constexpr int PER = UNIT / static_cast<int>(sizeof(T));
+    struct alignas(UNIT) Pack {
+      T v[PER];
+    };
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    l[v] = lane + 32 * v < experts ? to_f32(row[lane + 32 * v]) : -INFINITY;
+    for (int u = 0; u < V / PER; ++u) {
+      Pack p;
+      if (e < experts) p = reinterpret_cast<const Pack*>(row + e)[u];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) l[u * PER + i] = e < experts ? to_f32(p.v[i]) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = e + v < experts ? to_f32(row[e + v]) : -INFINITY;
+  }
+}
+template <class T, int V, bool VEC>
+SGE_DEV void store_logits(T* row, int experts, int lane, const float (&l)[V]) {
+  const int e = lane * V;
+  if constexpr (VEC) {
+    constexpr int BYTES = V * static_cast<int>(sizeof(T));
+    constexpr int UNIT = BYTES >= 16 ? 16 : BYTES;
+    constexpr int PER = UNIT / static_cast<int>(sizeof(T));
+    struct alignas(UNIT) Pack {
+      T v[PER];
+    };
+    if (e >= experts) return;
+#pragma unroll
+    for (int u = 0; u < V / PER; ++u) {
+      Pack p;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) from_f32(l[u * PER + i], &p.v[i]);
+      reinterpret_cast<Pack*>(row + e)[u] = p;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (e + v < experts) from_f32(l[v], row + e + v);
+  }
+}
+
+// Sorts a lane's V keys, largest first (V = 1, 2, 4, 8: Batcher's networks).
+SGE_DEV void sort2(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+template <int V>
+SGE_DEV void sort_keys(uint32_t (&k)[V]) {
+  if constexpr (V == 2) sort2(k[0], k[1]);
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int h = 0; h < V; h += 4) {
+      sort2(k[h], k[h + 1]);
+      sort2(k[h + 2], k[h + 3]);
+      sort2(k[h], k[h + 2]);
+      sort2(k[h + 1], k[h + 3]);
+      sort2(k[h + 1], k[h + 2]);
+    }
+  }
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sort2(k[i], k[i + 4]);
+    sort2(k[2], k[4]);
+    sort2(k[3], k[5]);
+    sort2(k[1], k[2]);
+    sort2(k[3], k[4]);
+    sort2(k[5], k[6]);
+  }
+}
+
+// The K largest of a row's values l: lane j < K gets the j-th one's expert and
+// value (-1 where no expert is left); returns the largest value's key.
+template <class T, int V>
+SGE_DEV uint32_t top_k(const float (&l)[V], int K, int lane, int& my_id, float& my_value) {
+  uint32_t key[V], top = 0;
+  if constexpr (sizeof(T) == 2) {
+    // A bf16 leaves the low half of its key free for the expert, so one
+    // maximum finds value and index (complemented: ties go to the lower one),
+    // and with a lane's keys sorted taking one is a shift: E = 256, k = 8 took
+    // 1.6 times as long as with the general form below.
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = (order_key(l[v]) & 0xffff0000u) | (0xffffu - (lane * V + v));
+    sort_keys<V>(key);
+    uint32_t mine = 0;
+    for (int j = 0; j < K; ++j) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, key[0]);
+      if (j == 0) top = m;
+      if ((m | 0xffffu) <= kKeyMinusInf) break;  // no expert left
+      if (lane == j) mine = m;
+      if (key[0] == m) {
+#pragma unroll
+        for (int v = 0; v + 1 < V; ++v) key[v] = key[v + 1];
+        key[V - 1] = 0;
+      }
+    }
+    if (mine) {
+      my_id = static_cast<int>(0xffffu - (mine & 0xffffu));
+      // the value's own bits: the low half of a bf16's pattern is zero (ones
+      // in the key of a negative number)
+      my_value = key_value((mine & 0x80000000u) ? (mine & 0xffff0000u) : (mine | 0xffffu));
+    }
+    return (top & 0x80000000u) ? (top & 0xffff0000u) : (top | 0xffffu);
+  } else {
+    uint32_t best = 0, my_key = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      key[v] = order_key(l[v]);
+      best = max(best, key[v]);
+    }
+    for (int j = 0; j < K; ++j) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+      if (j == 0) top = m;
+      if (m <= kKeyMinusInf) break;  // no expert left
+      const int owner = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
+      // the owner's first value equal to m is taken; its best is then the
+      // largest that is left
+      int at = 0;
+      if (lane == owner) {
+        best = 0;
+        bool taken = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const bool here = key[v] == m && !taken;
+          if (here) at = v;
+          taken |= here;
+          key[v] = here ? 0 : key[v];
+          best = max(best, key[v]);
+        }
+      }
+      const int id = owner * V + __shfl_sync(0xffffffffu, at, owner);
+      if (lane == j) {
+        my_id = id;
+        my_key = m;
+      }
+    }
+    if (my_key) my_value = key_value(my_key);
+    return top;
+  }
 }
 
 // Rows of block b, warp by warp: choose, weigh, count.
-template <class T, int V>
+template <class T, int V, bool VEC>
 SGE_DEV void route_choose(const T* __restrict__ logits, const RouteArgs& a, int b, int* hist, float* psum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = a.experts, K = a.top_k;
-  for (int i = threadIdx.x; i <= E; i += kRouteThreads) hist[i] = 0;
-  __syncthreads();
   const int64_t first = (static_cast<int64_t>(b) * kRouteWarps + warp) * a.rows_per_warp;
   const int64_t last = first + a.rows_per_warp < a.n ? first + a.rows_per_warp : a.n;
+  float next[V];
+  int next_live = 0;
+  const auto fetch = [&](int64_t row) {
+    if (row >= last) return;
+    next_live = a.mask ? a.mask[row] : 1;
+    load_logits<T, V, VEC>(logits + row * E, E, lane, next);
+  };
+  fetch(first);
+  for (int i = threadIdx.x; i <= E; i += kRouteThreads) hist[i] = 0;
+  __syncthreads();
   float p[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) p[v] = 0.0f;
   int live = 0;
   for (int64_t row = first; row < last; ++row) {
+    float l[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = next[v];
+    const bool is_live = next_live != 0;
+    fetch(row + 1);  // in flight while this row is worked on
     int my_id = -1;
     float my_w = 0.0f;
-    if (!a.mask || a.mask[row]) {
-      float l[V];
-      load_logits<T, V>(logits + row * E, E, lane, l);
-      uint32_t key[V];
+    if (is_live) {
       bool bad = false;  // a NaN or +inf among the logits
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        bad |= !(l[v] < INFINITY);
-        key[v] = order_key(l[v]);
-      }
+      for (int v = 0; v < V; ++v) bad |= !(l[v] < INFINITY);
       if (__any_sync(0xffffffffu, bad)) {
         // routed nowhere; its probabilities, and with them the loss, are NaN
         ++live;
 #pragma unroll
         for (int v = 0; v < V; ++v) p[v] = __uint_as_float(0x7fffffffu);
       } else {
-        uint32_t top = 0, my_key = kKeyMinusInf;
-        for (int j = 0; j < K; ++j) {
-          uint32_t best = 0;
-          int at = 0;
-#pragma unroll
-          for (int v = V - 1; v >= 0; --v)
-            if (key[v] >= best) {
-              best = key[v];
-              at = v;
-            }
-          const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-          if (j == 0) top = m;
-          if (m <= kKeyMinusInf) break;  // no expert left
-          const int id = __reduce_min_sync(0xffffffffu, best == m ? lane + 32 * at : 0x7fffffff);
-          if (lane == j) {
-            my_id = id;
-            my_key = m;
-          }
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (id == lane + 32 * v) key[v] = 0;
-        }
+        float my_value = 0.0f;
+        const uint32_t top = top_k<T, V>(l, K, lane, my_id, my_value);
         if (top > kKeyMinusInf) {
           ++live;
           const float high = key_value(top);
@@ -133,7 +263,7 @@ SGE_DEV void route_choose(const T* __restrict__ logits, const RouteArgs& a, int 
           const float inv = 1.0f / warp_sum(sum);
 #pragma unroll
           for (int v = 0; v < V; ++v) p[v] += e[v] * inv;
-          const float mine = my_id >= 0 ? expf(key_value(my_key) - high) : 0.0f;
+          const float mine = my_id >= 0 ? expf(my_value - high) : 0.0f;
           my_w = a.renorm ? mine / warp_sum(mine) : mine * inv;
           if (my_id >= 0) atomicAdd(&hist[my_id], 1);
         }
@@ -147,7 +277,7 @@ SGE_DEV void route_choose(const T* __restrict__ logits, const RouteArgs& a, int 
   if (lane == 0) atomicAdd(&hist[E], live);
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (lane + 32 * v < E) psum[warp * E + lane + 32 * v] = p[v];
+    if (lane * V + v < E) psum[warp * E + lane * V + v] = p[v];
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kRouteThreads) {
     float s = 0.0f;
@@ -159,79 +289,119 @@ SGE_DEV void route_choose(const T* __restrict__ logits, const RouteArgs& a, int 
 }
 
 // Places of block b's assignments; block 0 also writes counts, offsets and
-// the loss.  smem: hist [kRouteWarps][E].
+// the loss.  smem: hist [kRouteWarps][E + 1] (the odd pitch keeps a column's
+// cells in different banks).
 SGE_DEV void route_place(const RouteArgs& a, int b, int* hist) {
-  __shared__ int s_total[4][kMaxExperts + 1], s_before[4][kMaxExperts];
+  __shared__ int s_total[4][kMaxExperts], s_before[4][kMaxExperts], s_live;
+  __shared__ double s_p[4][kMaxExperts];
+  __shared__ int s_at[kMaxExperts];
   __shared__ int wsum[33];
   __shared__ double s_loss[kRouteWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int E = a.experts, K = a.top_k;
-  // counts of every expert over all blocks, and over the blocks before this one
+  const int E = a.experts, K = a.top_k, pitch = E + 1;
+  // this block's ids: a lane's of its warp's first rows stay in registers
+  const int64_t first = (static_cast<int64_t>(b) * kRouteWarps + warp) * a.rows_per_warp;
+  const int64_t last = first + a.rows_per_warp < a.n ? first + a.rows_per_warp : a.n;
+  constexpr int KEEP = 4;
+  int kept[KEEP];
+#pragma unroll
+  for (int r = 0; r < KEEP; ++r) kept[r] = lane < K && first + r < last ? a.ids[(first + r) * K + lane] : -1;
+  // counts of every expert over all blocks, and over the blocks before this
+  // one, in four parts (every fourth block), loads in batches
   const int part = threadIdx.x >> 8, e = threadIdx.x & 255;
-  for (int c = e; c <= E; c += 256) {
+  constexpr int BATCH = 19;  // half of a part of kRouteBlocks
+  if (e < E) {
     int total = 0, before = 0;
-#pragma unroll 8
-    for (int i = part; i < a.blocks; i += 4) {
-      const int v = a.part_count[static_cast<int64_t>(i) * (E + 1) + c];
-      total += v;
-      before += i < b ? v : 0;
+    for (int i0 = part; i0 < a.blocks; i0 += 4 * BATCH) {
+      int v[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        v[i] = i0 + 4 * i < a.blocks ? a.part_count[static_cast<int64_t>(i0 + 4 * i) * (E + 1) + e] : 0;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        total += v[i];
+        before += i0 + 4 * i < b ? v[i] : 0;
+      }
     }
-    s_total[part][c] = total;
-    if (c < E) s_before[part][c] = before;
+    s_total[part][e] = total;
+    s_before[part][e] = before;
   }
-  for (int i = threadIdx.x; i < kRouteWarps * E; i += kRouteThreads) hist[i] = 0;
+  if (b == 0 && e < E) {
+    double p = 0.0;
+    for (int i0 = part; i0 < a.blocks; i0 += 4 * BATCH) {
+      float v[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        v[i] = i0 + 4 * i < a.blocks ? a.part_p[static_cast<int64_t>(i0 + 4 * i) * E + e] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) p += v[i];
+    }
+    s_p[part][e] = p;
+  }
+  const int block_live =
+      b == 0 && threadIdx.x < a.blocks ? a.part_count[static_cast<int64_t>(threadIdx.x) * (E + 1) + E] : 0;
+  if (threadIdx.x == 0) s_live = 0;
+  for (int i = threadIdx.x; i < kRouteWarps * pitch; i += kRouteThreads) hist[i] = 0;
   __syncthreads();
+  if (block_live) atomicAdd(&s_live, block_live);
   const bool mine = threadIdx.x < E;
   int count = 0;
   if (mine)
     count = s_total[0][threadIdx.x] + s_total[1][threadIdx.x] + s_total[2][threadIdx.x] + s_total[3][threadIdx.x];
+#pragma unroll
+  for (int r = 0; r < KEEP; ++r)
+    if (kept[r] >= 0) atomicAdd(&hist[warp * pitch + kept[r]], 1);
+  for (int64_t i = (first + KEEP) * K + lane; i < last * K; i += 32) {
+    const int id = a.ids[i];
+    if (id >= 0) atomicAdd(&hist[warp * pitch + id], 1);
+  }
   int all;
   const int begin = block_scan_exclusive(count, wsum, &all);
-  // this block's assignments, by warp and expert
-  const int64_t first = (static_cast<int64_t>(b) * kRouteWarps + warp) * a.rows_per_warp;
-  const int64_t last = first + a.rows_per_warp < a.n ? first + a.rows_per_warp : a.n;
-  for (int64_t i = first * K + lane; i < last * K; i += 32) {
-    const int id = a.ids[i];
-    if (id >= 0) atomicAdd(&hist[warp * E + id], 1);
-  }
+  if (mine)
+    s_at[threadIdx.x] = begin + s_before[0][threadIdx.x] + s_before[1][threadIdx.x] + s_before[2][threadIdx.x] +
+                        s_before[3][threadIdx.x];
   __syncthreads();
-  if (mine) {
-    int at = begin + s_before[0][threadIdx.x] + s_before[1][threadIdx.x] + s_before[2][threadIdx.x] +
-             s_before[3][threadIdx.x];
-    for (int w = 0; w < kRouteWarps; ++w) {
-      const int c = hist[w * E + threadIdx.x];
-      hist[w * E + threadIdx.x] = at;
-      at += c;
+  // where each warp's assignments of an expert begin: one warp per expert, a
+  // lane per warp, a prefix sum over the lanes
+  for (int c = warp; c < E; c += kRouteWarps) {
+    const int n = hist[lane * pitch + c];
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
     }
+    hist[lane * pitch + c] = s_at[c] + incl - n;
   }
   __syncthreads();
   // row by row: a row's experts are distinct, so its lanes touch distinct cells
-  for (int64_t row = first; row < last; ++row) {
+  const auto place = [&](int64_t row, int id) {
     if (lane < K) {
       const int64_t i = row * K + lane;
-      const int id = a.ids[i];
       int at = -1;
       if (id >= 0) {
-        at = hist[warp * E + id]++;
+        at = hist[warp * pitch + id]++;
         a.order[at] = static_cast<int32_t>(i);
       }
       a.pos[i] = at;
     }
     __syncwarp();
-  }
+  };
+#pragma unroll
+  for (int r = 0; r < KEEP; ++r)
+    if (first + r < last) place(first + r, kept[r]);
+  for (int64_t row = first + KEEP; row < last; ++row) place(row, lane < K ? a.ids[row * K + lane] : -1);
   // no assignment behind the last one
   for (int64_t i = all + static_cast<int64_t>(b) * kRouteThreads + threadIdx.x; i < a.n * K;
        i += static_cast<int64_t>(a.blocks) * kRouteThreads)
     a.order[i] = -1;
   if (b) return;
-  const int live = s_total[0][E] + s_total[1][E] + s_total[2][E] + s_total[3][E];
+  const int live = s_live;
   double term = 0.0;
   if (mine) {
     a.counts[threadIdx.x] = count;
     a.offsets[threadIdx.x] = begin;
-    double p = 0.0;
-    for (int i = 0; i < a.blocks; ++i) p += a.part_p[static_cast<int64_t>(i) * E + threadIdx.x];
-    term = p * count;
+    term = ((s_p[0][threadIdx.x] + s_p[1][threadIdx.x]) + (s_p[2][threadIdx.x] + s_p[3][threadIdx.x])) * count;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
@@ -247,28 +417,28 @@ SGE_DEV void route_place(const RouteArgs& a, int b, int* hist) {
   }
 }
 
-template <class T, int V>
+template <class T, int V, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads, 1) route_choose_kernel(const T* logits, const RouteArgs a) {
-  extern __shared__ int smem[];
+  extern __shared__ __align__(16) int smem[];
   grid_dep_wait();
   grid_dep_launch();
-  route_choose<T, V>(logits, a, blockIdx.x, smem, reinterpret_cast<float*>(smem + a.experts + 1));
+  route_choose<T, V, VEC>(logits, a, blockIdx.x, smem, reinterpret_cast<float*>(smem + a.experts + 1));
 }
 
 __global__ void __launch_bounds__(kRouteThreads, 1) route_place_kernel(const RouteArgs a) {
-  extern __shared__ int smem[];
+  extern __shared__ __align__(16) int smem[];
   grid_dep_wait();
   grid_dep_launch();
   route_place(a, blockIdx.x, smem);
 }
 
 // Few rows: one block does both.
-template <class T, int V>
+template <class T, int V, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads, 1) route_one_kernel(const T* logits, const RouteArgs a) {
-  extern __shared__ int smem[];
+  extern __shared__ __align__(16) int smem[];
   grid_dep_wait();
   grid_dep_launch();
-  route_choose<T, V>(logits, a, 0, smem, reinterpret_cast<float*>(smem + a.experts + 1));
+  route_choose<T, V, VEC>(logits, a, 0, smem, reinterpret_cast<float*>(smem + a.experts + 1));
   __syncthreads();
   route_place(a, 0, smem);
 }
@@ -292,12 +462,15 @@ struct RouteGradArgs {
 // * f_e / live.  Raw weights add dw_j at ids_j; then dl = p (dp - <p, dp>).
 // Renormalised weights are a softmax over the chosen logits: they add
 // w_j (dw_j - <w, dw>) to dl at ids_j.
-template <class T, int V>
+template <class T, int V, bool VEC>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const T* __restrict__ logits, const RouteGradArgs a,
                                                         T* __restrict__ dlogits) {
+  // per warp: what the weights' gradient adds at each of a row's experts
+  __shared__ __align__(16) float s_at[8][32 * V];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
+  float* row_at = s_at[threadIdx.x >> 5];
   const int E = a.experts, K = a.top_k;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
   float share[V];
@@ -306,15 +479,23 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const T* __restrict__ lo
     const double d = a.dloss ? static_cast<double>(*a.dloss) * E / (live * all) : 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      share[v] = lane + 32 * v < E ? static_cast<float>(d * a.counts[lane + 32 * v]) : 0.0f;
+      share[v] = lane * V + v < E ? static_cast<float>(d * a.counts[lane * V + v]) : 0.0f;
   }
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < a.n; row += warps) {
-    float dl[V];
+    float dl[V], l[V];
+    load_logits<T, V, VEC>(logits + row * E, E, lane, l);
+    int id = -1;
+    float g = 0.0f, w = 0.0f;
+    if (lane < K && a.dw) {
+      id = a.ids[row * K + lane];
+      g = a.dw[row * K + lane];
+      w = a.w[row * K + lane];
+    }
+    if (id < 0) g = w = 0.0f;  // whatever dw holds there
 #pragma unroll
     for (int v = 0; v < V; ++v) dl[v] = 0.0f;
     if (!a.mask || a.mask[row]) {
-      float l[V], high = -INFINITY;
-      load_logits<T, V>(logits + row * E, E, lane, l);
+      float high = -INFINITY;
       bool bad = false;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -333,15 +514,6 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const T* __restrict__ lo
           sum += p[v];
         }
         const float inv = 1.0f / warp_sum(sum);
-        int id = -1;
-        float g = 0.0f, w = 0.0f;
-        if (lane < K && a.dw) {
-          id = a.ids[row * K + lane];
-          if (id >= 0) {
-            g = a.dw[row * K + lane];
-            w = a.w[row * K + lane];
-          }
-        }
         if (a.renorm) g = w * (g - warp_sum(w * g));
         float dp[V], at[V];
 #pragma unroll
@@ -350,14 +522,17 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const T* __restrict__ lo
           dp[v] = share[v];
           at[v] = 0.0f;
         }
-        if (a.dw)
-          for (int j = 0; j < K; ++j) {
-            const int idj = __shfl_sync(0xffffffffu, id, j);
-            const float gj = __shfl_sync(0xffffffffu, g, j);
+        if (a.dw) {
+          // a row's experts are distinct: its lanes write distinct cells
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-              if (idj == lane + 32 * v) at[v] += gj;
-          }
+          for (int v = 0; v < V; ++v) row_at[lane * V + v] = 0.0f;
+          __syncwarp();
+          if (static_cast<uint32_t>(id) < static_cast<uint32_t>(E)) row_at[id] = g;
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < V; ++v) at[v] = row_at[lane * V + v];
+          __syncwarp();
+        }
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -372,9 +547,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const T* __restrict__ lo
         }
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (lane + 32 * v < E) from_f32(dl[v], dlogits + row * E + lane + 32 * v);
+    store_logits<T, V, VEC>(dlogits + row * E, E, lane, dl);
   }
 }
 
@@ -385,26 +558,33 @@ static int route_blocks(int64_t n) {
   return static_cast<int>(b < 1 ? 1 : b < kRouteBlocks ? b : kRouteBlocks);
 }
 
-template <class T, int V>
-static int route_fwd(const void* logits, RouteArgs& a, cudaStream_t st) {
+template <class T, int V, bool VEC>
+static int route_fwd_as(const void* logits, RouteArgs& a, cudaStream_t st) {
   const T* l = static_cast<const T*>(logits);
-  const size_t smem = (static_cast<size_t>(kRouteWarps + 1) * a.experts + 1) * 4;
-  if (a.blocks == 1) {
-    const int rc = set_smem_limit(reinterpret_cast<const void*>(route_one_kernel<T, V>), static_cast<int>(smem));
-    if (rc) return rc;
-    return launch_pdl(route_one_kernel<T, V>, dim3(1), dim3(kRouteThreads), smem, st, "moe_route_fwd", l, a);
-  }
-  const int rc = launch_pdl(route_choose_kernel<T, V>, dim3(a.blocks), dim3(kRouteThreads), smem, st,
+  const size_t smem = static_cast<size_t>(kRouteWarps + 1) * (a.experts + 1) * 4;
+  const void* last = a.blocks == 1 ? reinterpret_cast<const void*>(route_one_kernel<T, V, VEC>)
+                                   : reinterpret_cast<const void*>(route_place_kernel);
+  int rc = set_smem_limit(last, static_cast<int>(smem));  // with its static share it may pass 48 KB
+  if (rc) return rc;
+  if (a.blocks == 1)
+    return launch_pdl(route_one_kernel<T, V, VEC>, dim3(1), dim3(kRouteThreads), smem, st, "moe_route_fwd", l, a);
+  rc = launch_pdl(route_choose_kernel<T, V, VEC>, dim3(a.blocks), dim3(kRouteThreads), smem, st,
                             "moe_route_fwd (choose)", l, a);
   if (rc) return rc;
   return launch_pdl(route_place_kernel, dim3(a.blocks), dim3(kRouteThreads), smem, st, "moe_route_fwd (place)", a);
 }
 
 template <class T, int V>
+static int route_fwd(const void* logits, RouteArgs& a, cudaStream_t st) {
+  return a.experts % V == 0 ? route_fwd_as<T, V, true>(logits, a, st) : route_fwd_as<T, V, false>(logits, a, st);
+}
+
+template <class T, int V>
 static int route_bwd(const void* logits, const RouteGradArgs& a, void* dlogits, cudaStream_t st) {
   const int64_t want = (a.n + 7) / 8, most = 8 * static_cast<int64_t>(sm_count());
-  return launch_pdl(route_bwd_kernel<T, V>, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(256), 0,
-                    st, "moe_route_bwd", static_cast<const T*>(logits), a, static_cast<T*>(dlogits));
+  auto kern = a.experts % V == 0 ? route_bwd_kernel<T, V, true> : route_bwd_kernel<T, V, false>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(256), 0, st, "moe_route_bwd",
+                    static_cast<const T*>(logits), a, static_cast<T*>(dlogits));
 }
 
 static int check_route(const char* fn, int64_t n, int experts, int top_k, int dtype) {

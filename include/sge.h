@@ -499,8 +499,8 @@ int twell_gate_pack_int8(const int8_t* xq, int64_t ldx, const float* sx, const i
  *   pos[n][j]   the place of assignment (n, j) in expert order: expert by
  *               expert, tokens ascending within one; order[pos] = n * top_k + j
  *   loss        E * sum_e (counts[e] / sum counts) * (mean over live tokens of p_e)
- * A token is live unless its mask byte is 0 (its logits are then not read) or
- * all its logits are -infinity.  An expert whose logit is -infinity is never
+ * A token is live unless its mask byte is 0 (whatever its logits hold) or all
+ * its logits are -infinity.  An expert whose logit is -infinity is never
  * chosen.  Where no expert is left, ids and pos are -1 and w is 0; order is -1
  * behind the last assignment.  A live token with a NaN or +infinity among its
  * logits is routed nowhere and makes the loss NaN.
@@ -524,7 +524,7 @@ int moe_route_fwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int
  *   dlogits = p (dp - <p, dp>)   [+ w_j (dw_j - <w, dw>) at ids_j, renorm != 0]
  * mask, ids, w, counts, offsets and n_live as given to and by moe_route_fwd;
  * dloss fp32 [1] on the device or NULL (0); dw fp32 [N][top_k] or NULL (0;
- * entries whose id is -1 are not read).  dlogits [N][E] in the logits' dtype:
+ * entries whose id is -1 have no effect).  dlogits [N][E] in the logits' dtype:
  * 0 for tokens that are not live, NaN for live ones that are not finite.
  */
 int moe_route_bwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int n_experts, int top_k,

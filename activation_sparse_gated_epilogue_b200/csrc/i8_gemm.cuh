@@ -29,8 +29,12 @@ constexpr int kMaxGroups = 256;
 constexpr int64_t kI8MaxK = 133000;        // k * 127 * 127 stays below 2^31
 constexpr int64_t kI8MaxRows = 1LL << 30;  // row and column indices of a tile stay 32-bit
 
-template <int BN_, int NB_, int NACC_, int HALVES_, bool PAIR_, bool PER_BLOCK_ = false>
+// GROUPED: the engine takes group bounds.  STAGING: bytes of shared memory per
+// epilogue warp.
+template <int BN_, int NB_, int NACC_, int HALVES_, bool PAIR_, bool GROUPED_, bool PER_BLOCK_, int STAGING_>
 struct I8Shape {
+  static constexpr bool GROUPED = GROUPED_;
+  static constexpr int STAGING = STAGING_;
   static constexpr int BN = BN_, NB = NB_, NACC = NACC_, HALVES = HALVES_;
   static constexpr bool PAIR = PAIR_, PER_BLOCK = PER_BLOCK_;
   // warps before the epilogue's: 2, or a warpgroup of 4 where registers move
@@ -48,12 +52,15 @@ struct I8Shape {
   static constexpr int A_BYTES = kBM * kI8BK;
   static constexpr int B_BYTES = B_ROWS * kI8BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_LOADS * B_BYTES;
-  static constexpr int STAGES = (196 * 1024) / STAGE_BYTES > 8 ? 8 : (196 * 1024) / STAGE_BYTES;
+  static constexpr int STAGING_BYTES = 4 * HALVES * STAGING;
+  // the stage ring takes what is left of 227 KB (2 KB of it: the tile list)
+  static constexpr int RING = 227 * 1024 - (GROUPED ? 2304 : 256) - 1024 - 512 - STAGING_BYTES;
+  static constexpr int STAGES = RING / STAGE_BYTES > 8 ? 8 : RING / STAGE_BYTES;
   static constexpr int ACC_COLS = BN * NB;
   static constexpr int USED_COLS = NACC * ACC_COLS;
   static constexpr int TMEM_COLS = USED_COLS <= 32 ? 32 : USED_COLS <= 64 ? 64 : USED_COLS <= 128 ? 128
                                    : USED_COLS <= 256 ? 256 : 512;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 /*align slack*/ + 512 /*barriers*/;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 /*align slack*/ + 512 /*barriers*/;
   static_assert(USED_COLS <= 512, "TMEM columns");
   static_assert(MMA_N % (PAIR ? 32 : 16) == 0 && MMA_N <= 256, "UMMA N");
   static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "1024-byte aligned sub-tiles");
@@ -79,8 +86,9 @@ struct I8Tile {
 // The tile list, built in shared memory from the group bounds.
 template <class Shape>
 struct I8Sched {
-  int off[kMaxGroups + 1];    // clamped group bounds
-  int first[kMaxGroups + 1];  // row blocks before group g
+  static constexpr int GROUPS = Shape::GROUPED ? kMaxGroups : 1;
+  int off[GROUPS + 1];    // clamped group bounds
+  int first[GROUPS + 1];  // row blocks before group g
 
   // one whole warp
   __device__ __forceinline__ void build(const I8Problem& p, int lane) {
@@ -180,6 +188,64 @@ SGE_DEV void i8_commit(uint64_t* bar) {
   else umma_commit(bar);
 }
 
+// Rows of 128 bytes from one warp's staging memory to global memory.  A lane
+// holds one row of a tile, but 32 rows' 16-byte stores are 32 lines each; via
+// shared memory (16-byte pieces swizzled by row, so that neither side has bank
+// conflicts) a store covers four whole rows, and where the matrix's pitch leaves
+// rows unaligned, 32 neighbouring elements.
+template <class T>
+struct StagedRows {
+  static constexpr int COLS = 128 / static_cast<int>(sizeof(T));  // columns at a time
+  static constexpr int PER = 16 / static_cast<int>(sizeof(T));
+
+  SGE_DEV static uint8_t* piece(uint8_t* stage, int row, int p) { return stage + row * 128 + ((p ^ (row & 7)) * 16); }
+
+  // this lane's row: columns [c, c + W) of the 128 bytes
+  template <int W>
+  SGE_DEV static void put(uint8_t* stage, int lane, int c, const float (&v)[W]) {
+#pragma unroll
+    for (int j = 0; j < W; j += PER) {
+      uint32_t w[4];
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = static_cast<uint32_t>(f32_to_bf16_bits(v[j + 2 * i])) |
+                 (static_cast<uint32_t>(f32_to_bf16_bits(v[j + 2 * i + 1])) << 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[j + i]);
+      }
+      *reinterpret_cast<uint4*>(piece(stage, lane, (c + j) / PER)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+
+  // all lanes: rows [row0, row0 + 32) (those below row_end) of a matrix of
+  // `pitch` columns, its columns [col0, col0 + COLS) (those below pitch)
+  SGE_DEV static void flush(uint8_t* stage, int lane, T* out, int64_t row0, int64_t row_end, int col0, int pitch) {
+    __syncwarp();
+    if (pitch % PER == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + lane / 8, p = lane % 8;
+        const uint4 v = *reinterpret_cast<const uint4*>(piece(stage, r, p));
+        const int col = col0 + p * PER;
+        if (row0 + r < row_end && col < pitch) *reinterpret_cast<uint4*>(out + (row0 + r) * pitch + col) = v;
+      }
+    } else {
+#pragma unroll 4
+      for (int r = 0; r < 32; ++r) {
+        if (row0 + r >= row_end) break;
+#pragma unroll
+        for (int c = lane; c < COLS; c += 32) {
+          const T v = reinterpret_cast<const T*>(piece(stage, r, c / PER))[c % PER];
+          if (col0 + c < pitch) out[(row0 + r) * pitch + col0 + c] = v;
+        }
+      }
+    }
+    __syncwarp();
+  }
+};
+
 // Arrive on a barrier of another CTA of the cluster.  CTA scope: what it
 // orders is this warp's tensor-memory reads, done before the tcgen05 fence in
 // front of it; cluster scope would also wait for the warp's global stores and
@@ -192,10 +258,13 @@ SGE_DEV void mbar_arrive_remote(uint32_t cluster_addr) {
 // lanes, its first column), this thread's row and its tile.
 struct I8Out {
   uint32_t taddr;
-  int64_t row;  // row of A of this thread
-  bool row_ok;  // inside the tile's group
+  int64_t row;      // row of A of this thread
+  int64_t row_end;  // end of the tile's group
+  bool row_ok;      // row < row_end
+  int lane;
   int col0;     // first column (within the group) of this warp's share
   int group, split;
+  uint8_t* stage;  // this warp's staging memory
 };
 
 // W floats of one row to out (rounded to its type), of which `left` lie inside
@@ -242,7 +311,8 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
   __shared__ I8Sched<Shape> sched;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * Shape::STAGE_BYTES);
+  uint8_t* staging = smem + STAGES * Shape::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + Shape::STAGING_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tmem_full = empty + STAGES;
   uint64_t* tmem_empty = tmem_full + NACC;
@@ -407,7 +477,10 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
       if (tc.kb0 >= tc.kb1) continue;  // an empty split (the epilogue's reader skips it too)
       I8Out o;
       o.row = static_cast<int64_t>(tc.row0) + rank * kBM + quarter * 32 + lane;
+      o.row_end = tc.row_end;
       o.row_ok = o.row < tc.row_end;
+      o.lane = lane;
+      o.stage = staging + (warp - Shape::FIRST_EPI) * Shape::STAGING;
       o.col0 = tc.col0 + half * COLS;
       o.group = tc.group;
       o.split = tc.split;

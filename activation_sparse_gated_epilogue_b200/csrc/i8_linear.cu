@@ -74,14 +74,19 @@ struct EpiI8Linear {
 
   template <int COLS>
   __device__ __forceinline__ void run(const I8Out& o, int n) const {
+    using Rows = StagedRows<T>;
+    static_assert(COLS % Rows::COLS == 0, "whole rows of 128 bytes");
     const float s = o.row_ok ? __ldg(sx + o.row) : 0.0f;
 #pragma unroll 1
-    for (int ch = 0; ch < COLS / 32; ++ch) {
-      const int col0 = o.col0 + ch * 32;
-      if (col0 >= n) break;
-      float v[32];
-      i8_scaled32(o.taddr + ch * 32, s, sw, col0, n, v);
-      if (o.row_ok) store_cols<32>(y + o.row * n + col0, v, n - col0, n);
+    for (int c = 0; c < COLS; c += Rows::COLS) {
+      if (o.col0 + c >= n) break;
+#pragma unroll
+      for (int part = 0; part < Rows::COLS; part += 32) {
+        float v[32];
+        i8_scaled32(o.taddr + c + part, s, sw, o.col0 + c + part, n, v);
+        Rows::put(o.stage, o.lane, part, v);
+      }
+      Rows::flush(o.stage, o.lane, y, o.row - o.lane, o.row_end, o.col0 + c, n);
     }
   }
 };
@@ -174,8 +179,8 @@ static int linear(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* 
                   const float* sw, void* y, int64_t n, int64_t m, int64_t k, int32_t* diag, cudaStream_t st) {
   const EpiI8Linear<T> epi{static_cast<T*>(y), sx, sw};
   if (n <= kSmallI8Rows)
-    return i8_product<I8Shape<64, 1, 2, 1, false>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st, "int8_linear");
-  return i8_product<I8Shape<256, 1, 2, 2, true>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st,
+    return i8_product<I8Shape<64, 1, 2, 1, false, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st, "int8_linear");
+  return i8_product<I8Shape<256, 1, 2, 2, true, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st,
                                                  "int8_linear (CTA pairs)");
 }
 
@@ -185,9 +190,9 @@ static int gate(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* wq
                 int32_t* diag, cudaStream_t st) {
   const EpiI8Twell<T> epi{count, idx, static_cast<uint16_t*>(val), cap, diag, sx, sw};
   if (n <= kSmallI8Rows)
-    return i8_product<I8Shape<128, 1, 2, 1, false>>(xq, ldx, wq, ldw, n, f, k, epi, diag, st,
+    return i8_product<I8Shape<128, 1, 2, 1, false, false, false, 0>>(xq, ldx, wq, ldw, n, f, k, epi, diag, st,
                                                     "twell_gate_pack_int8");
-  return i8_product<I8Shape<256, 1, 2, 2, true>>(xq, ldx, wq, ldw, n, f, k, epi, diag, st,
+  return i8_product<I8Shape<256, 1, 2, 2, true, false, false, 0>>(xq, ldx, wq, ldw, n, f, k, epi, diag, st,
                                                  "twell_gate_pack_int8 (CTA pairs)");
 }
 

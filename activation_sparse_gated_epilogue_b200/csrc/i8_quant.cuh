@@ -83,11 +83,12 @@ SGE_DEV void store_q(int8_t* dst, const float (&f)[8], float inv) {
       make_uint2(quant_pack4(f[0], f[1], f[2], f[3], inv), quant_pack4(f[4], f[5], f[6], f[7], inv));
 }
 
-// One warp quantises one row of `cols` values.  The row's quantised bytes
-// (zero-padded to ldq) go to each of the `copies` rows dst[] of q.  VEC: the
-// row is 16-byte aligned and cols a multiple of a 16-byte vector; otherwise
-// element by element.  Up to KEEP vectors a lane stay in registers between
-// the two passes; longer rows are read again (from L1 / L2).
+// One warp quantises one row of `cols` values: emit(c, f, inv) gets the values
+// f of columns c, c + 1, ... (zeros past the row) to be multiplied by inv and
+// rounded.  VEC: the row is 16-byte aligned and cols a multiple of a 16-byte
+// vector; otherwise it is read element by element.  Up to KEEP vectors a lane
+// stay in registers between the two passes; longer rows are read again (from
+// L1 / L2).
 template <class T, bool VEC, int KEEP, class Emit>
 SGE_DEV void quant_row(const T* x, int cols, int lane, uint32_t& amax_out, Emit&& emit) {
   using V = Vec16<T>;
@@ -127,14 +128,35 @@ SGE_DEV void quant_row(const T* x, int cols, int lane, uint32_t& amax_out, Emit&
       emit(v * V::N, f, inv);
     }
   } else {
-    for (int c = lane; c < cols; c += 32) amax = max(amax, abs_bits(to_f32(x[c])));
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    const float inv = quant_scale(amax).inv;
-    for (int c = 4 * lane; c < cols; c += 128) {
-      float f[4];
+    // four consecutive elements a lane, kept like the vectors above
+    const auto four = [&](int i, float (&f)[4]) {
+      const int c = 4 * (lane + 32 * i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[j] = c + j < cols ? to_f32(x[c + j]) : 0.0f;
-      emit(c, f, inv);
+    };
+    const int n4 = (cols + 3) / 4;
+    float keep[KEEP][4];
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) four(i, keep[i]);
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = max(amax, abs_bits(keep[i][j]));
+    for (int i = KEEP; 32 * i < n4; ++i) {
+      float f[4];
+      four(i, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = max(amax, abs_bits(f[j]));
+    }
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    const float inv = quant_scale(amax).inv;
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+      if (lane + 32 * i < n4) emit(4 * (lane + 32 * i), keep[i], inv);
+    for (int v = lane + 32 * KEEP; v < n4; v += 32) {
+      float f[4];
+      four((v - lane) / 32, f);
+      emit(4 * v, f, inv);
     }
   }
   amax_out = amax;

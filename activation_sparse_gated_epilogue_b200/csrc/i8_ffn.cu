@@ -15,10 +15,9 @@
 // exact; the blocks are scaled and added in fp32.
 #include "i8_gemm.cuh"
 #include "i8_quant.cuh"
+#include "i8_small.cuh"
 
 namespace sge {
-
-constexpr int kHGroup = 128;  // hidden units that share a scale
 
 // ------------------------------------------- quantise and order the tokens
 
@@ -121,14 +120,18 @@ struct EpiI8Down {
   const float* hs;
   const float* sd;
 
-  __device__ __forceinline__ float block_scale(const I8Out& o, int kb) const {
-    return o.row_ok ? hs[static_cast<int64_t>(kb) * rows + o.row] : 0.0f;
+  // this thread's row's scales, one every scale_pitch() floats (rows past the
+  // group's: some row's, their sums are not stored)
+  __device__ __forceinline__ const float* block_scales(const I8Out& o) const {
+    return hs + (o.row < rows ? o.row : rows - 1);
   }
+  __device__ __forceinline__ int64_t scale_pitch() const { return rows; }
 
   template <int COLS>
   __device__ __forceinline__ void store(const I8Out& o, const float (&sum)[COLS], int n) const {
     const float* cd = sd + static_cast<int64_t>(o.group) * n;
-    T* out = z + (o.split * rows + o.row) * n + o.col0;
+    using Rows = StagedRows<T>;
+    T* out = z + o.split * rows * n;
 #pragma unroll
     for (int c = 0; c < COLS; c += 32) {
       // all scales of 32 columns first: one latency, not one per store (n % 8
@@ -137,14 +140,17 @@ struct EpiI8Down {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         sc[j] = __ldg(reinterpret_cast<const float4*>(cd + min(o.col0 + c + 4 * j, n - 4)));
+      float v[32];
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        const float4 a = sc[j / 4], b = sc[j / 4 + 1];
-        const float* f = &sum[c + j];
-        const float v[8] = {f[0] * a.x, f[1] * a.y, f[2] * a.z, f[3] * a.w,
-                            f[4] * b.x, f[5] * b.y, f[6] * b.z, f[7] * b.w};
-        if (o.row_ok && o.col0 + c + j < n) store_cols<8>(out + c + j, v, 8, 8);
+      for (int j = 0; j < 8; ++j) {
+        v[4 * j] = sum[c + 4 * j] * sc[j].x;
+        v[4 * j + 1] = sum[c + 4 * j + 1] * sc[j].y;
+        v[4 * j + 2] = sum[c + 4 * j + 2] * sc[j].z;
+        v[4 * j + 3] = sum[c + 4 * j + 3] * sc[j].w;
       }
+      Rows::put(o.stage, o.lane, c % Rows::COLS, v);
+      if ((c + 32) % Rows::COLS == 0)
+        Rows::flush(o.stage, o.lane, out, o.row - o.lane, o.row_end, o.col0 + c + 32 - Rows::COLS, n);
     }
   }
 };
@@ -197,6 +203,7 @@ static int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
 struct FfnPlan {
   int64_t rows;     // assignments: n, or n * k
+  bool small;       // the kernels for a few tokens
   bool pairs;       // CTA-pair tiles
   int splits;       // parts of the down projection's K
   bool combine;     // y is summed from z by the combine kernel
@@ -207,17 +214,19 @@ struct FfnPlan {
 
 using GateUpPair = I8Shape<128, 2, 2, 1, true, true, false, 0>;
 using GateUpOne = I8Shape<128, 2, 2, 1, false, true, false, 0>;
-using DownPair = I8Shape<256, 1, 2, 2, true, true, true, 0>;
-using DownOne = I8Shape<128, 1, 4, 2, false, true, true, 0>;
+using DownPair = I8Shape<256, 1, 2, 2, true, true, true, 4096>;
+using DownOne = I8Shape<128, 1, 4, 2, false, true, true, 4096>;
 
 static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype, bool routed) {
   FfnPlan p = {};
   p.rows = routed ? n * k : n;
+  // a few tokens whose quantised rows fit a block's shared memory
+  p.small = n <= kSmallTokens && kSmallTokens * round16(d) <= 128 * 1024;
   // 256-row tiles when an expert has more rows than that on average
   p.pairs = p.rows / e > 256;
   p.splits = 1;
   const int64_t kb = (f + kI8BK - 1) / kI8BK;
-  if (!p.pairs) {
+  if (!p.pairs && !p.small) {
     // few output tiles: cut K so that about every SM (of 148) has one, at
     // least 4 blocks (512 hidden units) each, no part empty
     const int64_t groups = e < p.rows ? e : p.rows;  // experts that can have rows
@@ -229,7 +238,7 @@ static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype
     const int64_t per = (kb + s - 1) / s;
     p.splits = static_cast<int>((kb + per - 1) / per);
   }
-  p.combine = routed || p.splits > 1;
+  p.combine = !p.small && (routed || p.splits > 1);
   p.z_f32 = p.splits > 1 || dtype == SGE_F32;
   p.ldx = round16(d);
   p.ldh = round16(f);
@@ -290,7 +299,26 @@ static int ffn_combine(const FfnArgs& a, const FfnPlan& p) {
 }
 
 template <class T>
+static int ffn_small(const FfnArgs& a, const FfnPlan& p) {
+  const SmallFfn s = {a.n,  static_cast<int>(a.d), static_cast<int>(a.f), a.e, a.k, p.ldx, p.ldh, a.wg, a.wu, a.wd,
+                      a.sg, a.su, a.sd, a.w, a.offsets, a.pos, reinterpret_cast<int8_t*>(a.ws + p.hq),
+                      reinterpret_cast<float*>(a.ws + p.hs)};
+  const int nt = a.n == 1 ? 1 : a.n <= 4 ? 4 : 8;
+  auto kern = nt == 1 ? i8_small_up_kernel<T, 1> : nt == 4 ? i8_small_up_kernel<T, 4> : i8_small_up_kernel<T, 8>;
+  const int smem = static_cast<int>(nt * p.ldx);
+  int rc = set_smem_limit(reinterpret_cast<const void*>(kern), smem);
+  if (rc) return rc;
+  const int64_t used = a.e < p.rows ? a.e : p.rows;  // experts that can have rows
+  rc = launch_pdl(kern, dim3(static_cast<unsigned>((a.f + kHGroup - 1) / kHGroup), static_cast<unsigned>(used)),
+                  dim3(512), smem, a.st, "int8 ffn (gate, up; few tokens)", static_cast<const T*>(a.x), s);
+  if (rc) return rc;
+  return launch_pdl(i8_small_down_kernel<T>, dim3(static_cast<unsigned>((a.d + kDownChannels - 1) / kDownChannels)),
+                    dim3(512), 0, a.st, "int8 ffn (down; few tokens)", s, static_cast<T*>(a.y));
+}
+
+template <class T>
 static int ffn(const FfnArgs& a, const FfnPlan& p) {
+  if (p.small) return ffn_small<T>(a, p);
   int rc = launch_pdl(i8_dispatch_kernel<T>, dim3(static_cast<unsigned>((a.n + 7) / 8)), dim3(256), 0, a.st,
                       "int8 ffn (quantise)", static_cast<const T*>(a.x), a.n, static_cast<int>(a.d), a.k, a.pos,
                       static_cast<int>(p.rows), reinterpret_cast<int8_t*>(a.ws + p.xq), p.ldx,

@@ -52,7 +52,8 @@ struct I8Shape {
   static constexpr int A_BYTES = kBM * kI8BK;
   static constexpr int B_BYTES = B_ROWS * kI8BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_LOADS * B_BYTES;
-  static constexpr int STAGING_BYTES = 4 * HALVES * STAGING;
+  static constexpr int SCALES_AHEAD = PER_BLOCK ? 8 : 0;  // slots of block scales per epilogue thread
+  static constexpr int STAGING_BYTES = 4 * HALVES * STAGING + SCALES_AHEAD * 128 * HALVES * 4;
   // the stage ring takes what is left of 227 KB (2 KB of it: the tile list)
   static constexpr int RING = 227 * 1024 - (GROUPED ? 2304 : 256) - 1024 - 512 - STAGING_BYTES;
   static constexpr int STAGES = RING / STAGE_BYTES > 8 ? 8 : RING / STAGE_BYTES;
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* staging = smem + STAGES * Shape::STAGE_BYTES;
+  float* scales = reinterpret_cast<float*>(staging + 4 * Shape::HALVES * Shape::STAGING);
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + Shape::STAGING_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tmem_full = empty + STAGES;
@@ -430,6 +432,7 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
 #pragma unroll
             for (int k = 0; k < kI8BK / 32; ++k)
               umma_i8<PAIR>(d_tmem, adesc0 + at + 2 * k, bdesc0 + at + 2 * k, idesc, (!fresh || k != 0) ? 1u : 0u);
+            // frees the stage; PER_BLOCK it also says that the block's sums are there
             i8_commit<PAIR>(&empty[s]);
             if (!PER_BLOCK && kb == tc.kb1 - 1) i8_commit<PAIR>(&tmem_full[acc]);
           }
@@ -488,43 +491,48 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
         float sum[COLS];
 #pragma unroll
         for (int j = 0; j < COLS; ++j) sum[j] = 0.0f;
-        // four blocks' scales are loaded while the four before are added: a
-        // block takes a few hundred cycles, a load from L2 longer
-        constexpr int AHEAD = 4;
-        float next[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) next[i] = tc.kb0 + i < tc.kb1 ? epi.block_scale(o, tc.kb0 + i) : 0.0f;
-        for (int kb4 = tc.kb0; ok && kb4 < tc.kb1; kb4 += AHEAD) {
-          float scale[AHEAD];
-#pragma unroll
-          for (int i = 0; i < AHEAD; ++i) {
-            scale[i] = next[i];
-            const int kb = kb4 + AHEAD + i;
-            next[i] = kb < tc.kb1 ? epi.block_scale(o, kb) : 0.0f;
+        // The blocks' scales come by asynchronous copies to this thread's own
+        // slots, SCALES_AHEAD blocks early: a load from L2 takes longer than a
+        // block, and there are no registers left to hold values in flight.
+        constexpr int AHEAD = Shape::SCALES_AHEAD;
+        const uint32_t slots = smem_u32(scales + threadIdx.x - 32 * Shape::FIRST_EPI);
+        const float* src_scale = epi.block_scales(o);
+        const auto fetch = [&](int kb, int slot) {
+          if (kb < tc.kb1)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slots + slot * (128 * Shape::HALVES * 4)),
+                         "l"(src_scale + static_cast<int64_t>(kb) * epi.scale_pitch())
+                         : "memory");
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll 1
+        for (int i = 0; i < AHEAD; ++i) fetch(tc.kb0 + i, i);
+        int slot = 0;
+#pragma unroll 1
+        for (int kb = tc.kb0; kb < tc.kb1; ++kb) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+          float scale;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(scale) : "r"(slots + slot * (128 * Shape::HALVES * 4)) : "memory");
+          fetch(kb + AHEAD, slot);
+          slot = slot + 1 == AHEAD ? 0 : slot + 1;
+          // the commit that frees the block's stage also says that its sums are there
+          ok = __all_sync(0xffffffffu, wait_or_abort(&empty[s_done], s_ph, abort_flag, diag));
+          if (!ok) break;
+          if (++s_done == STAGES) {
+            s_done = 0;
+            s_ph ^= 1;
           }
+          tc_fence_after();
+          const uint32_t src = lane_base + acc * Shape::ACC_COLS;
+          uint32_t r[2][32];
+          tmem_ld32(src, r[0]);
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) {
-            if (kb4 + i >= tc.kb1) break;
-            // the commit that frees the block's stage also says that its sums are there
-            ok = __all_sync(0xffffffffu, wait_or_abort(&empty[s_done], s_ph, abort_flag, diag));
-            if (!ok) break;
-            if (++s_done == STAGES) {
-              s_done = 0;
-              s_ph ^= 1;
-            }
-            tc_fence_after();
-            const uint32_t src = lane_base + acc * Shape::ACC_COLS;
-            uint32_t r[2][32];
-            tmem_ld32(src, r[0]);
+          for (int ch = 0; ch < COLS / 32; ++ch) {
+            tmem_ld_wait();
+            if (ch + 1 < COLS / 32) tmem_ld32(src + (ch + 1) * 32, r[(ch + 1) & 1]);
+            else release();  // the block's last sums are in registers: the MMA may write over them
 #pragma unroll
-            for (int ch = 0; ch < COLS / 32; ++ch) {
-              tmem_ld_wait();
-              if (ch + 1 < COLS / 32) tmem_ld32(src + (ch + 1) * 32, r[(ch + 1) & 1]);
-              else release();  // the block's last sums are in registers: the MMA may write over them
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                sum[ch * 32 + j] = fmaf(__int2float_rn(static_cast<int>(r[ch & 1][j])), scale[i], sum[ch * 32 + j]);
-            }
+            for (int j = 0; j < 32; ++j)
+              sum[ch * 32 + j] = fmaf(__int2float_rn(static_cast<int>(r[ch & 1][j])), scale, sum[ch * 32 + j]);
           }
         }
         if (ok) epi.template store<COLS>(o, sum, p.n);

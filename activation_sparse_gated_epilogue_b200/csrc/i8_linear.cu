@@ -9,6 +9,7 @@
 // fp32 times the two scales, in this order, rounded once more to a bf16 y.
 #include "i8_gemm.cuh"
 #include "i8_quant.cuh"
+#include "i8_small.cuh"
 
 namespace sge {
 
@@ -177,6 +178,13 @@ static int i8_product(const int8_t* xq, int64_t ldx, const int8_t* wq, int64_t l
 template <class T>
 static int linear(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* wq, int64_t ldw,
                   const float* sw, void* y, int64_t n, int64_t m, int64_t k, int32_t* diag, cudaStream_t st) {
+  if (n <= kSmallTokens) {
+    auto kern = n == 1 ? i8_linear_small_kernel<T, 1> : n <= 4 ? i8_linear_small_kernel<T, 4>
+                                                               : i8_linear_small_kernel<T, 8>;
+    return launch_pdl(kern, dim3(static_cast<unsigned>((m + 7) / 8)), dim3(256), 0, st, "int8_linear (few tokens)",
+                      xq, ldx, sx, wq, ldw, sw, static_cast<T*>(y), static_cast<int>(n), static_cast<int>(m),
+                      static_cast<int>(k));
+  }
   const EpiI8Linear<T> epi{static_cast<T*>(y), sx, sw};
   if (n <= kSmallI8Rows)
     return i8_product<I8Shape<64, 1, 2, 1, false, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st, "int8_linear");

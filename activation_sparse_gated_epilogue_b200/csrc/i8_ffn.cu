@@ -220,10 +220,17 @@ using DownOne = I8Shape<128, 1, 4, 2, false, true, true, 4096>;
 static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype, bool routed) {
   FfnPlan p = {};
   p.rows = routed ? n * k : n;
-  // a few tokens whose quantised rows fit a block's shared memory
-  p.small = n <= kSmallTokens && kSmallTokens * round16(d) <= 128 * 1024;
-  // 256-row tiles when an expert has more rows than that on average
-  p.pairs = p.rows / e > 256;
+  // A few tokens whose quantised rows fit a block's shared memory, at most two
+  // for each expert that can have any: 2048 x 8192 without experts took 20 / 24
+  // / 31 us for 1 / 2 / 4 tokens there and 28 us on tiles; 32 experts of 1024 x
+  // 1024, 4 of them a token, 30 us for 8 tokens and 40 us on tiles.
+  p.small = n <= kSmallTokens && p.rows <= 2 * (e < p.rows ? e : p.rows) && kSmallTokens * round16(d) <= 128 * 1024;
+  // CTA pairs (256-row, 256-column tiles) when an expert has rows for more than
+  // two of them on average and the down product's tiles fill most of the 74
+  // pairs: 2048 x 8192 without experts took 70 / 111 us for 1024 / 1536 tokens
+  // on single CTAs and 80 / 93 us on pairs; 32 experts of 1024 x 1024 with 512
+  // rows each 125 and 135 us.
+  p.pairs = p.rows / e > 512 && (p.rows / 256) * ((d + 255) / 256) >= 40;
   p.splits = 1;
   const int64_t kb = (f + kI8BK - 1) / kI8BK;
   if (!p.pairs && !p.small) {

@@ -162,7 +162,8 @@ struct EpiI8Twell {
 
 // --------------------------------------------------------------- dispatch
 
-// Batches of at most this many rows run on single-CTA 128-row tiles.
+// Batches of at most this many rows run on single-CTA 128-row tiles (the gate
+// of 2048 x 8192 at 256 / 257 tokens: 18 / 29 us there, 25 us at 257 on pairs).
 constexpr int64_t kSmallI8Rows = 256;
 
 template <class Shape, class Epi>
@@ -178,18 +179,24 @@ static int i8_product(const int8_t* xq, int64_t ldx, const int8_t* wq, int64_t l
 template <class T>
 static int linear(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* wq, int64_t ldw,
                   const float* sw, void* y, int64_t n, int64_t m, int64_t k, int32_t* diag, cudaStream_t st) {
-  if (n <= kSmallTokens) {
-    auto kern = n == 1 ? i8_linear_small_kernel<T, 1> : n <= 4 ? i8_linear_small_kernel<T, 4>
-                                                               : i8_linear_small_kernel<T, 8>;
+  if (n <= kSmallLinear) {
+    auto kern = n == 1 ? i8_linear_small_kernel<T, 1> : i8_linear_small_kernel<T, 2>;
     return launch_pdl(kern, dim3(static_cast<unsigned>((m + 7) / 8)), dim3(256), 0, st, "int8_linear (few tokens)",
                       xq, ldx, sx, wq, ldw, sw, static_cast<T*>(y), static_cast<int>(n), static_cast<int>(m),
                       static_cast<int>(k));
   }
   const EpiI8Linear<T> epi{static_cast<T*>(y), sx, sw};
+  // 2048 x 8192, 128 / 256 / 257 tokens: 9.2 / 13.8 / 18.4 us on 64 columns a
+  // tile (more tiles for a batch of few rows), 9.9 / 10.2 / 15.0 us on 128,
+  // and 13.3 us at 257 on CTA pairs
+  if (n <= kBM)
+    return i8_product<I8Shape<64, 1, 2, 1, false, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st,
+                                                                       "int8_linear");
   if (n <= kSmallI8Rows)
-    return i8_product<I8Shape<64, 1, 2, 1, false, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st, "int8_linear");
+    return i8_product<I8Shape<128, 1, 2, 2, false, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st,
+                                                                        "int8_linear");
   return i8_product<I8Shape<256, 1, 2, 2, true, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st,
-                                                 "int8_linear (CTA pairs)");
+                                                                     "int8_linear (CTA pairs)");
 }
 
 template <int T>

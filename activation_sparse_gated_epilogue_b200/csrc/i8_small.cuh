@@ -1,8 +1,8 @@
-// The 8-bit operators for a few tokens (at most kSmallTokens): products of
-// weight rows with one to eight vectors, bound by the bytes of the weights.
-// CUDA cores (four products per __dp4a) instead of tensor-core tiles, whose
-// 128 rows would be mostly empty and whose column tiles leave SMs idle.
-// Integer sums, so any split of a row gives the same result.
+// The 8-bit operators for a few tokens: products of weight rows with a few
+// vectors, bound by the bytes of the weights.  CUDA cores (four products per
+// __dp4a) instead of tensor-core tiles, whose 128 rows would be mostly empty
+// and whose column tiles leave SMs idle.  Integer sums, so any split of a row
+// gives the same result.
 #pragma once
 
 #include "i8_gemm.cuh"
@@ -10,7 +10,10 @@
 
 namespace sge {
 
-constexpr int kSmallTokens = 8;
+constexpr int kSmallTokens = 8;  // of the feed-forward block, where experts leave each weight few of them
+// int8_linear: 2048 x 8192 took 5.2 / 8.4 / 10.8 us for 1 / 2 / 4 tokens here
+// and 8.8 us for any of these numbers on the tiles.
+constexpr int kSmallLinear = 2;
 constexpr int kHGroup = 128;  // hidden units of the feed-forward block that share a scale
 
 SGE_DEV int dot16(const uint4& a, const uint4& b, int acc) {
@@ -49,10 +52,13 @@ __global__ void __launch_bounds__(256) i8_linear_small_kernel(const int8_t* __re
                                                               int n, int m, int k) {
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int8_t* row = wq + static_cast<int64_t>(min(c, m - 1)) * ldw;
+  // towards L2 while the kernel before (the quantiser) still runs; what is
+  // read is read after the wait
+  for (int b = 128 * lane; b < k; b += 128 * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + b));
   grid_dep_wait();
   grid_dep_launch();
   if (c >= m) return;
-  const int8_t* row = wq + static_cast<int64_t>(c) * ldw;
   int acc[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) acc[t] = 0;
@@ -159,6 +165,10 @@ __global__ void __launch_bounds__(512, 1) i8_small_up_kernel(const T* __restrict
   const int8_t* wg = a.wg + (static_cast<int64_t>(e) * a.f + u0) * a.ldx;
   const int8_t* wu = a.wu + (static_cast<int64_t>(e) * a.f + u0) * a.ldx;
   const int units = min(kHGroup, a.f - u0);
+  if (threadIdx.x < 2)  // the block's weights on their way to L2 while its tokens are quantised
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(threadIdx.x ? wu : wg),
+                 "r"(static_cast<uint32_t>(units * a.ldx))
+                 : "memory");
   for (int r0 = lo; r0 < hi; r0 += NT) {
     const int nr = min(NT, hi - r0);
     if (warp < nr) {

@@ -68,7 +68,8 @@ def assert_close(y, want, mag, f, dtype, parts=None):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("n,d,f", [(1, 8, 8), (1, 256, 1024), (2, 264, 136), (5, 64, 128), (8, 512, 2048),
                                    (9, 200, 264), (33, 136, 520), (64, 256, 1024), (128, 512, 384),
-                                   (129, 256, 640), (257, 384, 896), (600, 264, 1000), (300, 1024, 256)])
+                                   (129, 256, 640), (257, 384, 896), (600, 264, 1000), (300, 1024, 256),
+                                   (2600, 1000, 264), (1300, 2048, 136)])
 def test_dense_block(cuda_device, dtype, n, d, f):
     rng = np.random.default_rng(n + d + f)
     ex = Experts(rng, 1, d, f, cuda_device)
@@ -117,7 +118,8 @@ def run_experts(cuda_device, n, d, f, e, k, dtype, ids=None, seed=0, x=None):
 @pytest.mark.parametrize("n,d,f,e,k", [(1, 64, 128, 2, 1), (1, 256, 512, 64, 8), (3, 136, 200, 5, 5),
                                        (4, 1024, 256, 32, 4), (17, 64, 136, 3, 2), (100, 256, 256, 8, 2),
                                        (300, 128, 384, 4, 2), (500, 264, 264, 256, 3), (1200, 128, 256, 3, 1),
-                                       (700, 256, 520, 2, 2)])
+                                       (700, 256, 520, 2, 2), (1300, 1544, 264, 2, 2), (2, 136, 264, 1, 1),
+                                       (8, 64, 264, 16, 4), (7, 72, 136, 100, 16)])
 def test_experts(cuda_device, dtype, n, d, f, e, k):
     y, want, mag, parts = run_experts(cuda_device, n, d, f, e, k, dtype)
     assert_close(y, want, mag, f, dtype, parts)

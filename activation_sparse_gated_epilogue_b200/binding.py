@@ -7,6 +7,7 @@ the current torch stream of the tensors' device unless ``stream`` is given.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -513,12 +514,13 @@ def _diag_ptr(diag: Optional[torch.Tensor], index: int) -> Optional[int]:
     return None if diag is None else _operand(diag, "diag", index, torch.int32, (4,))
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tensors allocated here but used on a stream other than the current
-    one: the allocator must not hand them out before that stream is done."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _allocating_on(stream):
+    """Tensors made for a call on `stream` come from that stream's pool: one
+    from the current stream's could still be in use there."""
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
+
+
+_NO_STREAM = contextlib.nullcontext()
 
 
 @dataclass
@@ -565,8 +567,8 @@ def int8_quant_rows(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None
         raise ValueError("x must have contiguous rows")
     ldx = x.stride(0) if n > 1 else d
     if out is None:
-        out = Int8Rows.empty(n, d, x.device)
-        _used_on(stream, out.q, out.scale)
+        with _allocating_on(stream):
+            out = Int8Rows.empty(n, d, x.device)
     q, ldq, scale = out._operands("out", index, n, d)
     _launch("int8_quant_rows", index, stream, x.data_ptr(), ldx, n, d, _dtype_code(x), q, ldq, scale)
     return out
@@ -583,8 +585,8 @@ def int8_linear(xq: Int8Rows, wq: Int8Rows, dtype: torch.dtype = torch.bfloat16,
     w, ldw, sw = wq._operands("wq", index, cols=k)
     n, m = xq.q.shape[0], wq.q.shape[0]
     if y is None:
-        y = torch.empty((n, m), dtype=dtype, device=xq.q.device)
-        _used_on(stream, y)
+        with _allocating_on(stream):
+            y = torch.empty((n, m), dtype=dtype, device=xq.q.device)
     _launch("int8_linear", index, stream, x, ldx, sx, w, ldw, sw, _operand(y, "y", index, dtype, (n, m)), n, m, k,
             _dtype_code(y), _diag_ptr(diag, index))
     return y
@@ -600,8 +602,8 @@ def twell_gate_pack_int8(xq: Int8Rows, wg_q: Int8Rows, tile: int, cap: int, out:
     w, ldw, sw = wg_q._operands("wg_q", index, cols=k)
     n, f = xq.q.shape[0], wg_q.q.shape[0]
     if out is None:
-        out = TwELL.empty(n, f, tile, cap, torch.bfloat16, xq.q.device)
-        _used_on(stream, out.count, out.idx, out.val)
+        with _allocating_on(stream):
+            out = TwELL.empty(n, f, tile, cap, torch.bfloat16, xq.q.device)
     _launch("twell_gate_pack_int8", index, stream, x, ldx, sx, w, ldw, sw, n, k, f, tile, cap,
             _operand(out.count, "count", index, torch.uint8, (n, f // tile)),
             _operand(out.idx, "idx", index, torch.uint8, (n, f // tile, cap)),
@@ -661,12 +663,12 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, renorm: bool = True, mask: O
     expert order, and the balance loss.  ``mask`` [N]: 0 for padding tokens."""
     index, n, e, x, m = _logits_operands(logits, mask)
     if out is None:
-        out = MoeRoute.empty(n, e, max(top_k, 0), logits.device)
-        _used_on(stream, out.ids, out.w, out.counts, out.offsets, out.pos, out.order, out.loss, out.n_live)
+        with _allocating_on(stream):
+            out = MoeRoute.empty(n, e, max(top_k, 0), logits.device)
     out.renorm = bool(renorm)
     if workspace is None:
-        workspace = moe_route_workspace(n, e, top_k, logits.device)
-        _used_on(stream, workspace)
+        with _allocating_on(stream):
+            workspace = moe_route_workspace(n, e, top_k, logits.device)
     i32, f32, nk = torch.int32, torch.float32, (n, top_k)
     _launch("moe_route_fwd", index, stream, x, m, n, e, top_k, int(out.renorm), _dtype_code(logits),
             _operand(out.ids, "ids", index, i32, nk), _operand(out.w, "w", index, f32, nk),
@@ -686,8 +688,8 @@ def moe_route_bwd(logits: torch.Tensor, route: MoeRoute, dloss: Optional[torch.T
     index, n, e, x, m = _logits_operands(logits, mask)
     k = route.ids.shape[1]
     if out is None:
-        out = torch.empty_like(logits)
-        _used_on(stream, out)
+        with _allocating_on(stream):
+            out = torch.empty_like(logits)
     i32, f32 = torch.int32, torch.float32
     _launch("moe_route_bwd", index, stream, x, m, n, e, k, int(route.renorm), _dtype_code(logits),
             _operand(route.ids, "ids", index, i32, (n, k)), _operand(route.w, "w", index, f32, (n, k)),
@@ -726,11 +728,11 @@ def _ffn_operands(x, index, wg_q, wu_q, wd_t_q, e, k, y, workspace, stream):
             raise ValueError(f"{name}.q must have rows of {(cols + 15) // 16 * 16} bytes, got {pitch}")
         weights += (q, scale)
     if y is None:
-        y = torch.empty_like(x)
-        _used_on(stream, y)
+        with _allocating_on(stream):
+            y = torch.empty_like(x)
     if workspace is None:
-        workspace = int8_ffn_workspace(n, d, f, e, k, x.dtype, x.device)
-        _used_on(stream, workspace)
+        with _allocating_on(stream):
+            workspace = int8_ffn_workspace(n, d, f, e, k, x.dtype, x.device)
     return n, d, f, weights, y, workspace
 
 

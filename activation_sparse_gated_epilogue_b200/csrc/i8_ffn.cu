@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256) i8_dispatch_kernel(const T* __restrict__ 
   if (row >= n) return;
   // place j of the token, or a number outside [0, rows)
   const auto place = [&](int j) -> uint32_t {
-    return pos ? static_cast<uint32_t>(__ldg(pos + row * k + j)) : static_cast<uint32_t>(row);
+    return pos ? checked_place(__ldg(pos + row * k + j), rows) : static_cast<uint32_t>(row);
   };
   uint32_t amax;
   quant_row<T, true, 8>(x + row * d, d, lane, amax, [&](int c, const auto& f, float inv) {
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(256) i8_combine_kernel(const Z* __restrict__ z
 #pragma unroll
   for (int j = 0; j < W; ++j) sum[j] = 0.0f;
   for (int a = 0; a < k; ++a) {
-    const uint32_t p = pos ? static_cast<uint32_t>(__ldg(pos + t * k + a)) : static_cast<uint32_t>(t);
+    const uint32_t p = pos ? checked_place(__ldg(pos + t * k + a), rows) : static_cast<uint32_t>(t);
     if (p >= static_cast<uint32_t>(rows)) continue;
     const float wt = w ? __ldg(w + t * k + a) : 1.0f;
     float part[W];

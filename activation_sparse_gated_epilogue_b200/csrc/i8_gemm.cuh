@@ -19,6 +19,7 @@
 #pragma once
 
 #include "i8_host.h"
+#include "i8_quant.cuh"
 #include "sge_host.h"
 #include "tc_gemm.cuh"
 
@@ -101,8 +102,8 @@ struct I8Sched {
       // an access out of range
       int hi = p.rows, begin = 0;
       if (p.offsets) {
-        hi = g < p.groups ? min(max(p.offsets[g + 1], 0), p.rows) : 0;
-        if (g == 0) begin = min(max(p.offsets[0], 0), p.rows);
+        hi = g < p.groups ? checked_bound(p.offsets[g + 1], 0, p.rows) : 0;
+        if (g == 0) begin = checked_bound(p.offsets[0], 0, p.rows);
         hi = max(hi, max(begin, floor));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -233,13 +234,12 @@ struct StagedRows {
         if (row0 + r < row_end && col < pitch) *reinterpret_cast<uint4*>(out + (row0 + r) * pitch + col) = v;
       }
     } else {
-#pragma unroll 4
+#pragma unroll 8
       for (int r = 0; r < 32; ++r) {
-        if (row0 + r >= row_end) break;
 #pragma unroll
         for (int c = lane; c < COLS; c += 32) {
           const T v = reinterpret_cast<const T*>(piece(stage, r, c / PER))[c % PER];
-          if (col0 + c < pitch) out[(row0 + r) * pitch + col0 + c] = v;
+          if (row0 + r < row_end && col0 + c < pitch) out[(row0 + r) * pitch + col0 + c] = v;
         }
       }
     }

@@ -4,6 +4,7 @@
 // kernel that quantises (and any restatement of it) gives the same integers.
 #pragma once
 
+#include "debug_checks.cuh"
 #include "sge_common.cuh"
 
 namespace sge {
@@ -42,6 +43,24 @@ SGE_DEV uint32_t quant_pack4(float a, float b, float c, float d, float inv) {
 }
 
 SGE_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// A place of a token's assignment: itself if it is one of `rows` places, else
+// a number that is not.  -1 means no place; others out of range are left out
+// too, and flagged by the debug build.
+SGE_DEV uint32_t checked_place(int32_t p, uint32_t rows) {
+#ifdef SGE_DEBUG
+  if (p != -1 && static_cast<uint32_t>(p) >= rows) debug_flag();
+#endif
+  return static_cast<uint32_t>(p) < rows ? static_cast<uint32_t>(p) : 0xffffffffu;
+}
+
+// A group bound, moved into [lo, rows].
+SGE_DEV int checked_bound(int b, int lo, int rows) {
+#ifdef SGE_DEBUG
+  if (b < lo || b > rows) debug_flag();
+#endif
+  return min(max(b, lo), rows);
+}
 
 // 16 bytes of an activation row as floats: 8 bf16 or 4 fp32.
 template <class T>

@@ -107,8 +107,8 @@ constexpr int kSmallRows = kSmallTokens * 16;  // places of at most kSmallTokens
 
 // Rows [*lo, *hi) of expert e, clamped like the tile engine's bounds.
 SGE_DEV void small_rows(const SmallFfn& a, int e, int rows, int* lo, int* hi) {
-  *lo = a.offsets ? min(max(a.offsets[e], 0), rows) : 0;
-  *hi = a.offsets ? min(max(a.offsets[e + 1], *lo), rows) : rows;
+  *lo = a.offsets ? checked_bound(a.offsets[e], 0, rows) : 0;
+  *hi = a.offsets ? checked_bound(a.offsets[e + 1], *lo, rows) : rows;
 }
 
 // The experts that have rows, in order (any block size; experts <= 256).
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(512, 1) i8_small_up_kernel(const T* __restrict
   small_rows(a, e, rows, &lo, &hi);
   if (a.pos) {
     for (int i = threadIdx.x; i < rows; i += 512) {
-      const uint32_t p = static_cast<uint32_t>(a.pos[i]);
+      const uint32_t p = checked_place(a.pos[i], rows);
       if (p < static_cast<uint32_t>(rows)) s_token[p] = i / a.k;
     }
     __syncthreads();
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(512) i8_small_down_kernel(const SmallFfn a, T*
   const int used = used_experts(a, rows, s_list, s_scratch);
   if (a.pos) {
     for (int i = threadIdx.x; i < rows; i += 512) {
-      const uint32_t p = static_cast<uint32_t>(a.pos[i]);
+      const uint32_t p = checked_place(a.pos[i], rows);
       if (p < static_cast<uint32_t>(rows)) {
         s_token[p] = i / a.k;
         s_w[p] = a.w[i];

@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const T* __restrict__ lo
 #pragma unroll
           for (int v = 0; v < V; ++v) row_at[lane * V + v] = 0.0f;
           __syncwarp();
-          if (static_cast<uint32_t>(id) < static_cast<uint32_t>(E)) row_at[id] = g;
+          if (checked_place(id, E) < static_cast<uint32_t>(E)) row_at[id] = g;
           __syncwarp();
 #pragma unroll
           for (int v = 0; v < V; ++v) at[v] = row_at[lane * V + v];

@@ -14,6 +14,7 @@
 #define SGE_WAIT_NS 20000000ull
 
 #include "../../../include/sge_selftest.h"
+#include "../i8_gemm.cuh"
 #include "../tc_launch.cuh"
 
 namespace sge {
@@ -27,6 +28,27 @@ struct EpiCountTiles {
   }
 };
 
+// The same for the 8-bit engine's epilogue interface.
+struct EpiCountI8 {
+  int* tiles_done;
+  template <int COLS>
+  __device__ __forceinline__ void run(const I8Out& o, int) const {
+    if (o.lane == 0) atomicAdd(tiles_done, 1);
+  }
+};
+
+// `b` read through a map whose box has half the rows that a stage expects.
+template <class Shape>
+static int i8_wait_timeout(const void* a, const void* b, int64_t m, int64_t n, int64_t k, const EpiCountI8& epi,
+                           int32_t* diag, cudaStream_t st) {
+  const I8Problem p{static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), 1, 1, nullptr};
+  I8Maps maps;
+  int rc = make_i8_maps<Shape>(&maps, p, static_cast<const int8_t*>(a), k, static_cast<const int8_t*>(b), nullptr, k);
+  if (!rc) rc = make_tmap_i8(&maps.b0, b, n, k, k, Shape::B_ROWS / 2);
+  if (rc) return rc;
+  return launch_i8_gemm<Shape>(maps, p, epi, diag, st, "selftest (8-bit engine)");
+}
+
 }  // namespace sge
 
 using namespace sge;
@@ -39,6 +61,12 @@ extern "C" int sge_selftest_wait_timeout(int pair, const void* a, const void* b,
     return fail(SGE_ERR_ARG, "sge_selftest_wait_timeout: bad arguments");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   EpiCountTiles epi{tiles_done};
+  if (pair == 2 || pair == 3) {  // the 8-bit engine: single CTA, CTA pair
+    if (k % 16) return fail(SGE_ERR_ARG, "sge_selftest_wait_timeout: bad arguments");
+    const EpiCountI8 e8{tiles_done};
+    return pair == 2 ? i8_wait_timeout<I8Shape<128, 1, 2, 1, false, false, false, 0>>(a, b, m, n, k, e8, diag, st)
+                     : i8_wait_timeout<I8Shape<256, 1, 2, 2, true, false, false, 0>>(a, b, m, n, k, e8, diag, st);
+  }
   CUtensorMap ma, mb;
   if (pair) {
     using S = TcPairShape<256, 1>;

@@ -141,6 +141,27 @@ def test_linear_row_that_is_not_finite_gives_nan(cuda_device):
     assert (y[1] == 0).all() and torch.isfinite(y[[0, 1, 3]]).all()
 
 
+def test_offsets_past_32_bits(cuda_device):
+    """Outputs and inputs of more than 2^31 elements: the last rows and
+    columns, and the first ones, which a wrapped offset would overwrite."""
+    n, d, m = 33000, 64, 66000
+    x = torch.randn(n, d, device=cuda_device)
+    w = torch.randn(m, d, device=cuda_device)
+    xq, wq = sge.int8_quant_rows(x), sge.int8_quant_rows(w)
+    y = sge.int8_linear(xq, wq, torch.bfloat16)
+    host = lambda r: (r.q.cpu().numpy(), r.scale.cpu().numpy())  # noqa: E731
+    (q, s), (p, t) = host(xq), host(wq)
+    for rows in (slice(0, 3), slice(16000, 16003), slice(n - 3, n)):
+        for cols in (slice(0, 300), slice(m - 300, m)):
+            assert_scaled(y[rows, cols], product64(q[rows], s[rows], p[cols], t[cols]), torch.bfloat16)
+    big = y[:, :65536].contiguous()                     # 2^31 elements and more to quantise
+    got = sge.int8_quant_rows(big)
+    for rows in (slice(0, 2), slice(n - 2, n)):
+        q, s = quant_np(big[rows].float().cpu().numpy())
+        np.testing.assert_array_equal(got.q[rows].cpu().numpy(), q)
+        np.testing.assert_array_equal(got.scale[rows].cpu().numpy(), s)
+
+
 def test_linear_empty_batch_and_repeats(cuda_device):
     wq = sge.int8_quant_rows(torch.randn(32, 64, device=cuda_device))
     x = sge.int8_quant_rows(torch.randn(300, 64, device=cuda_device))

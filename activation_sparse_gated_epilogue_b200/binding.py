@@ -7,7 +7,6 @@ the current torch stream of the tensors' device unless ``stream`` is given.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -514,45 +513,80 @@ def _diag_ptr(diag: Optional[torch.Tensor], index: int) -> Optional[int]:
     return None if diag is None else _operand(diag, "diag", index, torch.int32, (4,))
 
 
-def _allocating_on(stream):
+def _allocate(stream, make, *args):
     """Tensors made for a call on `stream` come from that stream's pool: one
     from the current stream's could still be in use there."""
-    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return make(*args)
+    with torch.cuda.stream(stream):
+        return make(*args)
 
 
-_NO_STREAM = contextlib.nullcontext()
+def _empty(shape, dtype, index: int) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
 
 
-@dataclass
 class Int8Rows:
     """An 8-bit matrix: q int8 [rows][pitch] (pitch a multiple of 16, bytes
     past `cols` are padding) and one fp32 scale per row.  Weights of E experts
     are E blocks of rows."""
-    q: torch.Tensor
-    scale: torch.Tensor
-    cols: int
+    __slots__ = ("cols", "_q", "_scale", "_buffer", "_shape")
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, cols: int):
+        self._q, self._scale, self.cols, self._buffer = q, scale, cols, None
 
     @staticmethod
     def empty(rows: int, cols: int, device) -> "Int8Rows":
-        return Int8Rows(torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=device),
-                        torch.empty(rows, dtype=torch.float32, device=device), cols)
+        """Uninitialised rows, the scales behind them in one allocation."""
+        out = Int8Rows.__new__(Int8Rows)
+        pitch = (cols + 15) & ~15
+        out.cols, out._shape = cols, (rows, pitch)
+        out._q = out._scale = None
+        out._buffer = torch.empty(rows * (pitch + 4), dtype=torch.int8, device=device)
+        return out
+
+    @property
+    def q(self) -> torch.Tensor:
+        if self._q is None:
+            n, pitch = self._shape
+            self._q = self._buffer[:n * pitch].view(n, pitch)
+        return self._q
+
+    @property
+    def scale(self) -> torch.Tensor:
+        if self._scale is None:
+            n, pitch = self._shape
+            self._scale = self._buffer[n * pitch:].view(torch.float32)
+        return self._scale
 
     @property
     def rows(self) -> int:
-        return self.q.shape[0]
+        return self.q.shape[0] if self._buffer is None else self._shape[0]
 
     def _operands(self, name: str, index: int, rows: Optional[int] = None, cols: Optional[int] = None):
-        """(address of q, pitch, address of scale), checked."""
-        q = self.q
-        if q.dim() != 2 or q.shape[1] % 16 or not 1 <= self.cols <= q.shape[1]:
-            raise ValueError(f"{name}.q must be [rows][pitch], pitch a multiple of 16, at least cols")
-        n, pitch = q.shape
+        """(address of q, pitch, address of scale, rows), checked."""
+        buffer = self._buffer
+        if buffer is not None:  # made by empty(): only its device and rows are in question
+            n, pitch = self._shape
+            if buffer.get_device() != index:
+                raise ValueError(f"{name} is on {buffer.device}, other operands on cuda:{index}")
+            q = buffer.data_ptr()
+            scale = q + n * pitch
+        else:
+            t = self._q
+            if t.dim() != 2 or t.shape[1] % 16 or not 1 <= self.cols <= t.shape[1]:
+                raise ValueError(f"{name}.q must be [rows][pitch], pitch a multiple of 16, at least cols")
+            n, pitch = t.shape
+            q = _operand(t, f"{name}.q", index, torch.int8, (n, pitch))
+            scale = _operand(self._scale, f"{name}.scale", index, torch.float32, (n,))
         if rows is not None and n != rows:
             raise ValueError(f"{name} must have {rows} rows, got {n}")
         if cols is not None and self.cols != cols:
             raise ValueError(f"{name} must have {cols} columns, got {self.cols}")
-        return (_operand(q, f"{name}.q", index, torch.int8, (n, pitch)), pitch,
-                _operand(self.scale, f"{name}.scale", index, torch.float32, (n,)))
+        return q, pitch, scale, n
+
+    def _index(self, name: str) -> int:
+        return _device_of(self._q if self._buffer is None else self._buffer, name)
 
 
 def int8_quant_rows(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None) -> Int8Rows:
@@ -567,9 +601,8 @@ def int8_quant_rows(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None
         raise ValueError("x must have contiguous rows")
     ldx = x.stride(0) if n > 1 else d
     if out is None:
-        with _allocating_on(stream):
-            out = Int8Rows.empty(n, d, x.device)
-    q, ldq, scale = out._operands("out", index, n, d)
+        out = _allocate(stream, Int8Rows.empty, n, d, x.device)
+    q, ldq, scale, _ = out._operands("out", index, n, d)
     _launch("int8_quant_rows", index, stream, x.data_ptr(), ldx, n, d, _dtype_code(x), q, ldq, scale)
     return out
 
@@ -579,14 +612,12 @@ def int8_linear(xq: Int8Rows, wq: Int8Rows, dtype: torch.dtype = torch.bfloat16,
                 stream=None) -> torch.Tensor:
     """y[n][m] = (sum over k of xq[n][k] * wq[m][k]) * xq.scale[n] * wq.scale[m]
     with exact integer sums, in bf16 or fp32."""
-    index = _device_of(xq.q, "xq")
+    index = xq._index("xq")
     k = xq.cols
-    x, ldx, sx = xq._operands("xq", index)
-    w, ldw, sw = wq._operands("wq", index, cols=k)
-    n, m = xq.q.shape[0], wq.q.shape[0]
+    x, ldx, sx, n = xq._operands("xq", index)
+    w, ldw, sw, m = wq._operands("wq", index, cols=k)
     if y is None:
-        with _allocating_on(stream):
-            y = torch.empty((n, m), dtype=dtype, device=xq.q.device)
+        y = _allocate(stream, _empty, (n, m), dtype, index)
     _launch("int8_linear", index, stream, x, ldx, sx, w, ldw, sw, _operand(y, "y", index, dtype, (n, m)), n, m, k,
             _dtype_code(y), _diag_ptr(diag, index))
     return y
@@ -596,14 +627,14 @@ def twell_gate_pack_int8(xq: Int8Rows, wg_q: Int8Rows, tile: int, cap: int, out:
                          diag: Optional[torch.Tensor] = None, stream=None) -> TwELL:
     """twell_gate_pack with the gate projection in 8-bit integers: TwELL
     (bf16 values) of ReLU of int8_linear's product."""
-    index = _device_of(xq.q, "xq")
+    index = xq._index("xq")
     k = xq.cols
-    x, ldx, sx = xq._operands("xq", index)
-    w, ldw, sw = wg_q._operands("wg_q", index, cols=k)
-    n, f = xq.q.shape[0], wg_q.q.shape[0]
+    x, ldx, sx, n = xq._operands("xq", index)
+    w, ldw, sw, f = wg_q._operands("wg_q", index, cols=k)
+    if tile < 1 or cap < 1:
+        raise ValueError(f"tile {tile} and cap {cap} must be at least 1")
     if out is None:
-        with _allocating_on(stream):
-            out = TwELL.empty(n, f, tile, cap, torch.bfloat16, xq.q.device)
+        out = _allocate(stream, TwELL.empty, n, f, tile, cap, torch.bfloat16, torch.device("cuda", index))
     _launch("twell_gate_pack_int8", index, stream, x, ldx, sx, w, ldw, sw, n, k, f, tile, cap,
             _operand(out.count, "count", index, torch.uint8, (n, f // tile)),
             _operand(out.idx, "idx", index, torch.uint8, (n, f // tile, cap)),
@@ -663,12 +694,10 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, renorm: bool = True, mask: O
     expert order, and the balance loss.  ``mask`` [N]: 0 for padding tokens."""
     index, n, e, x, m = _logits_operands(logits, mask)
     if out is None:
-        with _allocating_on(stream):
-            out = MoeRoute.empty(n, e, max(top_k, 0), logits.device)
+        out = _allocate(stream, MoeRoute.empty, n, e, max(top_k, 0), logits.device)
     out.renorm = bool(renorm)
     if workspace is None:
-        with _allocating_on(stream):
-            workspace = moe_route_workspace(n, e, top_k, logits.device)
+        workspace = _allocate(stream, moe_route_workspace, n, e, top_k, logits.device)
     i32, f32, nk = torch.int32, torch.float32, (n, top_k)
     _launch("moe_route_fwd", index, stream, x, m, n, e, top_k, int(out.renorm), _dtype_code(logits),
             _operand(out.ids, "ids", index, i32, nk), _operand(out.w, "w", index, f32, nk),
@@ -688,8 +717,7 @@ def moe_route_bwd(logits: torch.Tensor, route: MoeRoute, dloss: Optional[torch.T
     index, n, e, x, m = _logits_operands(logits, mask)
     k = route.ids.shape[1]
     if out is None:
-        with _allocating_on(stream):
-            out = torch.empty_like(logits)
+        out = _allocate(stream, torch.empty_like, logits)
     i32, f32 = torch.int32, torch.float32
     _launch("moe_route_bwd", index, stream, x, m, n, e, k, int(route.renorm), _dtype_code(logits),
             _operand(route.ids, "ids", index, i32, (n, k)), _operand(route.w, "w", index, f32, (n, k)),
@@ -723,16 +751,14 @@ def _ffn_operands(x, index, wg_q, wu_q, wd_t_q, e, k, y, workspace, stream):
     f = wg_q.rows // e
     weights = []
     for name, m, rows, cols in (("wg_q", wg_q, e * f, d), ("wu_q", wu_q, e * f, d), ("wd_t_q", wd_t_q, e * d, f)):
-        q, pitch, scale = m._operands(name, index, rows, cols)
+        q, pitch, scale, _ = m._operands(name, index, rows, cols)
         if pitch != (cols + 15) // 16 * 16:
             raise ValueError(f"{name}.q must have rows of {(cols + 15) // 16 * 16} bytes, got {pitch}")
         weights += (q, scale)
     if y is None:
-        with _allocating_on(stream):
-            y = torch.empty_like(x)
+        y = _allocate(stream, torch.empty_like, x)
     if workspace is None:
-        with _allocating_on(stream):
-            workspace = int8_ffn_workspace(n, d, f, e, k, x.dtype, x.device)
+        workspace = _allocate(stream, int8_ffn_workspace, n, d, f, e, k, x.dtype, x.device)
     return n, d, f, weights, y, workspace
 
 

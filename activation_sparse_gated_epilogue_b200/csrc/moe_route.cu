@@ -313,10 +313,10 @@ SGE_DEV void route_place(const RouteArgs& a, int b, int* hist) {
   if (e < E) {
     int total = 0, before = 0;
     for (int i0 = part; i0 < a.blocks; i0 += 4 * BATCH) {
+      const int32_t* src = a.part_count + i0 * (E + 1) + e;  // at most kRouteBlocks * 257: 32 bits do
       int v[BATCH];
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i)
-        v[i] = i0 + 4 * i < a.blocks ? a.part_count[static_cast<int64_t>(i0 + 4 * i) * (E + 1) + e] : 0;
+      for (int i = 0; i < BATCH; ++i) v[i] = i0 + 4 * i < a.blocks ? src[i * 4 * (E + 1)] : 0;
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
         total += v[i];
@@ -329,10 +329,10 @@ SGE_DEV void route_place(const RouteArgs& a, int b, int* hist) {
   if (b == 0 && e < E) {
     double p = 0.0;
     for (int i0 = part; i0 < a.blocks; i0 += 4 * BATCH) {
+      const float* src = a.part_p + i0 * E + e;
       float v[BATCH];
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i)
-        v[i] = i0 + 4 * i < a.blocks ? a.part_p[static_cast<int64_t>(i0 + 4 * i) * E + e] : 0.0f;
+      for (int i = 0; i < BATCH; ++i) v[i] = i0 + 4 * i < a.blocks ? src[i * 4 * E] : 0.0f;
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) p += v[i];
     }
@@ -432,10 +432,15 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_place_kernel(const Rou
   route_place(a, blockIdx.x, smem);
 }
 
-// Few rows: one block does both.
+// Few rows: one block does both, its counts and sums stay in shared memory.
 template <class T, int V, bool VEC>
-__global__ void __launch_bounds__(kRouteThreads, 1) route_one_kernel(const T* logits, const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, 1) route_one_kernel(const T* logits, const RouteArgs args) {
   extern __shared__ __align__(16) int smem[];
+  __shared__ int s_count[kMaxExperts + 1];
+  __shared__ float s_sum[kMaxExperts];
+  RouteArgs a = args;
+  a.part_count = s_count;
+  a.part_p = s_sum;
   grid_dep_wait();
   grid_dep_launch();
   route_choose<T, V, VEC>(logits, a, 0, smem, reinterpret_cast<float*>(smem + a.experts + 1));
@@ -475,11 +480,11 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const T* __restrict__ lo
   const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
   float share[V];
   {
-    const double live = max(*a.n_live, 1), all = max(a.offsets[E], 1);
-    const double d = a.dloss ? static_cast<double>(*a.dloss) * E / (live * all) : 0.0;
+    const float live = __int2float_rn(max(*a.n_live, 1)), all = __int2float_rn(max(a.offsets[E], 1));
+    const float d = a.dloss ? *a.dloss * E / live / all : 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      share[v] = lane * V + v < E ? static_cast<float>(d * a.counts[lane * V + v]) : 0.0f;
+      share[v] = lane * V + v < E ? d * __int2float_rn(a.counts[lane * V + v]) : 0.0f;
   }
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < a.n; row += warps) {
     float dl[V], l[V];

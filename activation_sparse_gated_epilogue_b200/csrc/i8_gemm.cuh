@@ -27,7 +27,7 @@ namespace sge {
 
 constexpr int kI8BK = 128;  // k per stage: one 128-byte swizzle row
 constexpr int kMaxGroups = 256;
-constexpr int64_t kI8MaxK = 133000;        // k * 127 * 127 stays below 2^31
+constexpr int64_t kI8MaxK = 131071;        // k * 128 * 128 stays below 2^31
 constexpr int64_t kI8MaxRows = 1LL << 30;  // row and column indices of a tile stay 32-bit
 
 // GROUPED: the engine takes group bounds.  STAGING: bytes of shared memory per
@@ -68,6 +68,9 @@ struct I8Shape {
   static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "1024-byte aligned sub-tiles");
   static_assert(HALVES == 1 || NB == 1, "column halves need one accumulator");
   static_assert(!PER_BLOCK || NB == 1, "per-block scales: one accumulator");
+  // PER_BLOCK epilogues wait on the stages' barriers: at most NACC blocks behind
+  // the MMAs, they must not miss a phase
+  static_assert(!PER_BLOCK || STAGES >= NACC, "stages");
 };
 
 struct I8Problem {
@@ -576,18 +579,47 @@ int make_i8_maps(I8Maps* m, const I8Problem& p, const int8_t* a, int64_t lda, co
   return rc;
 }
 
-// `max_m_blocks`: the most row blocks the call can have (with groups: their
-// rows rounded up), for the grid.
+// CTAs (PAIR: CTA pairs) of a kernel that can be resident at once, per device.
+template <class Shape, class Epi>
+int i8_workers() {
+  if constexpr (!Shape::PAIR) return sm_count();
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count() / 2;
+  if (cached[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sm_count() / 2));
+    cfg.blockDim = dim3(Shape::THREADS);
+    cfg.dynamicSmemBytes = Shape::SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const void* kern = reinterpret_cast<const void*>(i8_gemm_kernel<Shape, Epi>);
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = sm_count() / 2;
+    }
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
 template <class Shape, class Epi>
 int launch_i8_gemm(const I8Maps& m, const I8Problem& p, const Epi& epi, int32_t* diag, cudaStream_t st,
                    const char* what) {
   auto kern = i8_gemm_kernel<Shape, Epi>;
   int rc = set_smem_limit(reinterpret_cast<const void*>(kern), Shape::SMEM_BYTES);
   if (rc) return rc;
+  // the most row blocks there can be: with groups, one partial block more for each
   int64_t m_blocks = (p.rows + Shape::BM - 1) / Shape::BM;
-  if (p.offsets) m_blocks += p.groups - 1 < p.rows ? p.groups - 1 : p.rows;  // at most: one partial block a group
+  if (p.offsets) m_blocks += p.groups - 1 < p.rows ? p.groups - 1 : p.rows;
   const int64_t tiles = m_blocks * ((p.n + Shape::BN - 1) / Shape::BN) * p.splits;
-  const int64_t slots = Shape::PAIR ? sm_count() / 2 : sm_count();
+  const int64_t slots = i8_workers<Shape, Epi>();
   const int workers = static_cast<int>(tiles < slots ? tiles : slots);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(Shape::PAIR ? 2 * workers : workers);

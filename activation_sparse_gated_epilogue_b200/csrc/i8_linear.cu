@@ -235,8 +235,8 @@ extern "C" int int8_quant_rows(const void* x, int64_t ldx, int64_t n_rows, int64
     return fail(SGE_ERR_ARG, "int8_quant_rows: bad sizes rows=%lld cols=%lld", (long long)n_rows,
                 (long long)n_cols);
   if (dtype != SGE_BF16 && dtype != SGE_F32) return fail(SGE_ERR_UNSUPPORTED, "int8_quant_rows: dtype %d", dtype);
-  if (n_rows >= (1LL << 31) || n_cols >= (1LL << 31))
-    return fail(SGE_ERR_UNSUPPORTED, "int8_quant_rows: size beyond 2^31");
+  if (n_rows >= (1LL << 31) || n_cols >= (1LL << 30) || ldq >= (1LL << 30))
+    return fail(SGE_ERR_UNSUPPORTED, "int8_quant_rows: rows beyond 2^31, or a row beyond 2^30");
   if (ldx < n_cols) return fail(SGE_ERR_ARG, "int8_quant_rows: ldx below the row length");
   if (ldq < n_cols || ldq % 16)
     return fail(SGE_ERR_ARG, "int8_quant_rows: ldq must be a multiple of 16, at least the row length");

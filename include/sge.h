@@ -455,7 +455,8 @@ int sge_transpose_up_gate(const void* wu_t, const void* wg_t, void* w_ug, int64_
  *   q      int8 [n_rows][ldq]: columns n_cols .. ldq-1 are set to 0
  *   scale  fp32 [n_rows]
  * Errors: SGE_ERR_ARG for sizes below 0 (n_cols below 1), ldx < n_cols,
- * ldq < n_cols or ldq % 16; SGE_ERR_UNSUPPORTED for other dtypes.
+ * ldq < n_cols or ldq % 16; SGE_ERR_UNSUPPORTED for other dtypes, 2^31 rows,
+ * rows of 2^30 values.
  */
 int int8_quant_rows(const void* x, int64_t ldx, int64_t n_rows, int64_t n_cols, int dtype, int8_t* q,
                     int64_t ldq, float* scale, void* stream);
@@ -470,7 +471,7 @@ int int8_quant_rows(const void* x, int64_t ldx, int64_t n_rows, int64_t n_cols, 
  *   y   [n_tokens][n_out]  dtype (SGE_BF16 or SGE_F32), contiguous; any n_out
  * Bytes n_in .. ldx-1 (ldw-1) of a row are not part of the product.
  * Errors: SGE_ERR_ARG for bad sizes or pitches (ldx, ldw: multiples of 16, at
- * least n_in); SGE_ERR_UNSUPPORTED for n_in > 133000 (the sums would pass 32
+ * least n_in); SGE_ERR_UNSUPPORTED for n_in > 131071 (the sums could pass 32
  * bits), sizes of 2^30 and more, other dtypes.
  */
 int int8_linear(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* wq, int64_t ldw, const float* sw,
@@ -561,7 +562,7 @@ int moe_route_bwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int
  * int8_ffn_workspace_bytes for either call; n_experts = top_k = 1 for
  * int8_ffn_fwd) belongs to one call at a time.
  * Errors: SGE_ERR_ARG for bad sizes, d % 8, F % 8, top_k > E, a workspace too
- * small; SGE_ERR_UNSUPPORTED for d > 133000, E > 256, top_k > 16, other
+ * small; SGE_ERR_UNSUPPORTED for d > 131071, E > 256, top_k > 16, other
  * dtypes, N * top_k, E * F or E * d of 2^30 and more.
  */
 size_t int8_ffn_workspace_bytes(int64_t n_tokens, int64_t d_model, int64_t d_ff, int n_experts, int top_k,

@@ -233,6 +233,7 @@ def test_int8_quant_rejects_bad_arguments(lib):
     assert _quant(lib, scale=ctypes.c_void_p(4098)) == 1
     assert b"aligned" in lib.sge_last_error()
     assert _quant(lib, rows=1 << 31) == 2
+    assert _quant(lib, cols=1 << 30, ldx=1 << 30, ldq=1 << 30) == 2
 
 
 def _linear(lib, **kw):
@@ -253,7 +254,7 @@ def test_int8_linear_rejects_bad_arguments(lib):
     assert _linear(lib, ldx=72) == 1
     assert _linear(lib, ldw=68) == 1
     assert b"pitches" in lib.sge_last_error()
-    assert _linear(lib, k=133001, ldx=1 << 18, ldw=1 << 18) == 2
+    assert _linear(lib, k=131072, ldx=1 << 18, ldw=1 << 18) == 2
     assert b"32-bit sums" in lib.sge_last_error()
     assert _linear(lib, n=1 << 30) == 2
     assert _linear(lib, sw=None) == 1

@@ -129,6 +129,16 @@ def test_linear_extreme_integers_are_exact(cuda_device, n):
     assert torch.equal(y.cpu().double(), want.float().double())
 
 
+@pytest.mark.parametrize("n", [1, 2, 40, 300])
+def test_linear_longest_rows_of_the_lowest_integer(cuda_device, n):
+    """k = 131071 products of -128 * -128, the largest sum that is allowed."""
+    d, m = 131071, 40
+    low = lambda r: sge.Int8Rows(torch.full((r, d + 1), -128, dtype=torch.int8, device=cuda_device),  # noqa: E731
+                                 torch.ones(r, device=cuda_device), d)
+    y = sge.int8_linear(low(n), low(m), torch.float32)
+    assert (y.double() == torch.tensor(128.0 * 128 * d).float().double().item()).all()
+
+
 def test_linear_row_that_is_not_finite_gives_nan(cuda_device):
     x = torch.randn(5, 64, device=cuda_device)
     x[2, 7] = float("inf")

@@ -78,7 +78,7 @@ struct I8Problem {
   int n;       // output columns of a group (rows of B per group)
   int k;       // bytes of a row
   int groups;  // 1..kMaxGroups
-  int splits;  // K is cut into this many parts, each an output of its own
+  int splits;  // K is cut into this many parts, none empty, each an output of its own
   const int32_t* offsets;  // [groups + 1] row bounds on the device, or null (one group)
 };
 
@@ -477,10 +477,8 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
         acc_ph ^= 1;
       }
     };
-    bool ok = true;
-    for (int t = worker; ok && t < num_tiles; t += n_workers) {
-      const I8Tile tc = sched.tile(p, t, k_blocks);
-      if (tc.kb0 >= tc.kb1) continue;  // an empty split (the epilogue's reader skips it too)
+    // this thread's place in a tile
+    const auto place = [&](const I8Tile& tc) {
       I8Out o;
       o.row = static_cast<int64_t>(tc.row0) + rank * kBM + quarter * 32 + lane;
       o.row_end = tc.row_end;
@@ -490,32 +488,56 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
       o.col0 = tc.col0 + half * COLS;
       o.group = tc.group;
       o.split = tc.split;
+      return o;
+    };
+    // PER_BLOCK: the blocks' scales come by asynchronous copies to this thread's
+    // own slots, SCALES_AHEAD blocks early: a load from L2 takes longer than a
+    // block, and there are no registers left to hold values in flight.
+    constexpr int AHEAD = Shape::SCALES_AHEAD;
+    const uint32_t slots = smem_u32(scales + threadIdx.x - 32 * Shape::FIRST_EPI);
+    const auto fetch_scale = [&](const float* src, int kb, int kb1, int slot) {
+      if constexpr (PER_BLOCK) {
+        if (kb < kb1)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slots + slot * (128 * Shape::HALVES * 4)),
+                       "l"(src + static_cast<int64_t>(kb) * epi.scale_pitch())
+                       : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+    };
+    // the first scales of tile t (the tile before's are all used by then)
+    const auto fetch_first = [&](int t) {
+      if constexpr (PER_BLOCK) {
+        if (t >= num_tiles) return;
+        const I8Tile tc = sched.tile(p, t, k_blocks);
+        const float* src = epi.block_scales(place(tc));
+#pragma unroll 1
+        for (int i = 0; i < AHEAD; ++i) fetch_scale(src, tc.kb0 + i, tc.kb1, i);
+      }
+    };
+    bool ok = true;
+    // A single CTA fetches a tile's first scales before it stores the tile
+    // before (5-10% of the block where experts leave it short tiles); a pair as
+    // the tile begins: there the other order costs registers (171 -> 179 us for
+    // the down product at the 1B shape).
+    if (!PAIR) fetch_first(worker);
+    for (int t = worker; ok && t < num_tiles; t += n_workers) {
+      const I8Tile tc = sched.tile(p, t, k_blocks);  // no split is empty: the host sees to it
+      const I8Out o = place(tc);
+      // a warp whose rows all lie past the group's end only keeps the pace
+      const bool any = (PAIR && PER_BLOCK) || __any_sync(0xffffffffu, o.row_ok);
+      if (PAIR) fetch_first(t);
       if constexpr (PER_BLOCK) {
         float sum[COLS];
 #pragma unroll
         for (int j = 0; j < COLS; ++j) sum[j] = 0.0f;
-        // The blocks' scales come by asynchronous copies to this thread's own
-        // slots, SCALES_AHEAD blocks early: a load from L2 takes longer than a
-        // block, and there are no registers left to hold values in flight.
-        constexpr int AHEAD = Shape::SCALES_AHEAD;
-        const uint32_t slots = smem_u32(scales + threadIdx.x - 32 * Shape::FIRST_EPI);
         const float* src_scale = epi.block_scales(o);
-        const auto fetch = [&](int kb, int slot) {
-          if (kb < tc.kb1)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slots + slot * (128 * Shape::HALVES * 4)),
-                         "l"(src_scale + static_cast<int64_t>(kb) * epi.scale_pitch())
-                         : "memory");
-          asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-#pragma unroll 1
-        for (int i = 0; i < AHEAD; ++i) fetch(tc.kb0 + i, i);
         int slot = 0;
 #pragma unroll 1
         for (int kb = tc.kb0; kb < tc.kb1; ++kb) {
           asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
           float scale;
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(scale) : "r"(slots + slot * (128 * Shape::HALVES * 4)) : "memory");
-          fetch(kb + AHEAD, slot);
+          fetch_scale(src_scale, kb + AHEAD, tc.kb1, slot);
           slot = slot + 1 == AHEAD ? 0 : slot + 1;
           // the commit that frees the block's stage also says that its sums are there
           ok = __all_sync(0xffffffffu, wait_or_abort(&empty[s_done], s_ph, abort_flag, diag));
@@ -525,6 +547,10 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
             s_ph ^= 1;
           }
           tc_fence_after();
+          if (!any) {
+            release();
+            continue;
+          }
           const uint32_t src = lane_base + acc * Shape::ACC_COLS;
           uint32_t r[2][32];
           tmem_ld32(src, r[0]);
@@ -538,13 +564,18 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
               sum[ch * 32 + j] = fmaf(__int2float_rn(static_cast<int>(r[ch & 1][j])), scale, sum[ch * 32 + j]);
           }
         }
-        if (ok) epi.template store<COLS>(o, sum, p.n);
+        if (!ok) break;
+        if (!PAIR) fetch_first(t + n_workers);
+        if (any) epi.template store<COLS>(o, sum, p.n);
       } else {
         ok = __all_sync(0xffffffffu, wait_or_abort(&tmem_full[acc], acc_ph, abort_flag, diag));
         if (!ok) break;
         tc_fence_after();
-        o.taddr = lane_base + acc * Shape::ACC_COLS;
-        epi.template run<COLS>(o, p.n);
+        if (any) {
+          I8Out at = o;
+          at.taddr = lane_base + acc * Shape::ACC_COLS;
+          epi.template run<COLS>(at, p.n);
+        }
         release();
       }
     }

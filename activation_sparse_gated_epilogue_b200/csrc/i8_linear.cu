@@ -15,6 +15,9 @@ namespace sge {
 
 // ------------------------------------------------------------ quantisation
 
+// One warp per row: the row stays in registers between its maximum and its
+// rounding, so it is read once.  Bound by HBM: 16384 x 2560 bf16 (84 MB in, 42 MB
+// out) takes 25 us, 5.0 TB/s.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256) i8_quant_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows,
                                                        int cols, int8_t* __restrict__ q, int64_t ldq,
@@ -67,6 +70,10 @@ SGE_DEV void i8_scaled32(uint32_t taddr, float sx, const float* __restrict__ sw,
   }
 }
 
+// y's columns, 128 bytes of a row at a time through staging memory (16384 x 2560
+// x 10240 bf16: 276 us at full clocks, 3.1 POPS, against 340 us with each thread
+// storing its own row; the tensor pipe is busy 77% of the cycles, and in a
+// sustained run the power cap sets the time).
 template <class T>
 struct EpiI8Linear {
   T* y;
@@ -92,6 +99,9 @@ struct EpiI8Linear {
   }
 };
 
+// ReLU and the TwELL pack; each thread owns a row, so a tile's entries come out
+// in ascending order (8192 x 2048 x 8192 at 1% density: 87 us, 3.15 POPS, as fast
+// as the main loop alone).
 template <int T>
 struct EpiI8Twell {
   uint8_t* count;

@@ -11,8 +11,8 @@
 namespace sge {
 
 constexpr int kSmallTokens = 8;  // of the feed-forward block, where experts leave each weight few of them
-// int8_linear: 2048 x 8192 took 5.2 / 8.4 / 10.8 us for 1 / 2 / 4 tokens here
-// and 8.8 us for any of these numbers on the tiles.
+// int8_linear: 2048 x 8192 took 4.0 / 4.9 / 10.8 us for 1 / 2 / 4 tokens here and
+// 8.8 us for any of these numbers on the tiles.
 constexpr int kSmallLinear = 2;
 constexpr int kHGroup = 128;  // hidden units of the feed-forward block that share a scale
 
@@ -43,7 +43,7 @@ SGE_DEV uint4 load_weights(const int8_t* p) {
 // ------------------------------------------------------------- int8_linear
 
 // One warp per output channel, 16 bytes of its row a lane, four loads in
-// flight; NT tokens' rows come from L1.
+// flight; NT tokens' rows come from L1.  1 x 2048 -> 8192: 4.0 us (4.2 TB/s).
 template <class T, int NT>
 __global__ void __launch_bounds__(256) i8_linear_small_kernel(const int8_t* __restrict__ xq, int64_t ldx,
                                                               const float* __restrict__ sx,
@@ -137,7 +137,9 @@ SGE_DEV int used_experts(const SmallFfn& a, int rows, int* list, int* scratch) {
 
 // Gate and up projections, h and its quantisation: one block per used expert
 // and group of 128 hidden units, 16 warps of 8 units.  The block quantises its
-// tokens' rows itself (a launch less).  NT: rows of an expert at a time.
+// tokens' rows itself (a launch less).  NT: rows of an expert at a time.  With
+// the kernel below 18.7 us for one token of 2048 x 8192 (50 MB of weights), 10.8
+// us for one over four of 32 experts of 1024 x 1024.
 template <class T, int NT>
 __global__ void __launch_bounds__(512, 1) i8_small_up_kernel(const T* __restrict__ x, const SmallFfn a) {
   extern __shared__ __align__(16) int8_t s_x[];  // [NT][ldx]

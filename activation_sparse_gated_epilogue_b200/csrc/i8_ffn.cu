@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(256, 4)
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (col[u] < d) store_cols<W>(y + t * d + col[u], sum[u], W, W);
+    if (col[u] < d) store8(y + t * d + col[u], sum[u]);
 }
 
 // ------------------------------------------------------------------- host

@@ -271,39 +271,6 @@ struct I8Out {
   uint8_t* stage;  // this warp's staging memory
 };
 
-// W floats of one row to out (rounded to its type), of which `left` lie inside
-// the row; `pitch` (elements) tells whether 16-byte stores are aligned.
-template <int W>
-SGE_DEV void store_cols(__nv_bfloat16* out, const float (&v)[W], int left, int pitch) {
-  if (left >= W && pitch % 8 == 0) {
-#pragma unroll
-    for (int j = 0; j < W; j += 8) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = static_cast<uint32_t>(f32_to_bf16_bits(v[j + 2 * i])) |
-               (static_cast<uint32_t>(f32_to_bf16_bits(v[j + 2 * i + 1])) << 16);
-      *reinterpret_cast<uint4*>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      if (j < left) out[j] = __float2bfloat16_rn(v[j]);
-  }
-}
-template <int W>
-SGE_DEV void store_cols(float* out, const float (&v)[W], int left, int pitch) {
-  if (left >= W && pitch % 4 == 0) {
-#pragma unroll
-    for (int j = 0; j < W; j += 4)
-      *reinterpret_cast<float4*>(out + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      if (j < left) out[j] = v[j];
-  }
-}
-
 template <class Shape, class Epilogue>
 __global__ void __launch_bounds__(Shape::THREADS, 1)
     i8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,

@@ -88,6 +88,20 @@ struct Vec16<float> {
   }
 };
 
+// Eight values to a 16-byte aligned row.
+SGE_DEV void store8(__nv_bfloat16* out, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i])) |
+           (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i + 1])) << 16);
+  *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+SGE_DEV void store8(float* out, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 SGE_DEV float to_f32(float v) { return v; }
 SGE_DEV float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 SGE_DEV void from_f32(float v, float* o) { *o = v; }

@@ -645,27 +645,73 @@ def twell_gate_pack_int8(xq: Int8Rows, wg_q: Int8Rows, tile: int, cap: int, out:
 # ------------------------------------------------------------ expert router
 
 
-@dataclass
 class MoeRoute:
     """What moe_route_fwd gives (see include/sge.h): ids, w, pos [N][k]; order
     [N * k]; counts [E]; offsets [E + 1]; loss, n_live [1]; and the settings
     that its gradient needs again."""
-    ids: torch.Tensor
-    w: torch.Tensor
-    counts: torch.Tensor
-    offsets: torch.Tensor
-    pos: torch.Tensor
-    order: torch.Tensor
-    loss: torch.Tensor
-    n_live: torch.Tensor
-    renorm: bool = True
+    NAMES = ("ids", "w", "counts", "offsets", "pos", "order", "loss", "n_live")
+    __slots__ = ("renorm", "_tensors", "_buffer", "_sizes", "_at")
+
+    def __init__(self, ids, w, counts, offsets, pos, order, loss, n_live, renorm: bool = True):
+        self._tensors = [ids, w, counts, offsets, pos, order, loss, n_live]
+        self._buffer = None
+        self.renorm = renorm
 
     @staticmethod
     def empty(n_tokens: int, n_experts: int, top_k: int, device) -> "MoeRoute":
-        i = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)  # noqa: E731
-        f = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)  # noqa: E731
-        return MoeRoute(i(n_tokens, top_k), f(n_tokens, top_k), i(n_experts), i(n_experts + 1),
-                        i(n_tokens, top_k), i(n_tokens * top_k), f(1), i(1))
+        """Uninitialised tensors, views of one allocation."""
+        out = MoeRoute.__new__(MoeRoute)
+        out.renorm = True
+        out._tensors = [None] * 8
+        out._sizes = (n_tokens, n_experts, top_k)
+        nk = n_tokens * top_k
+        at, end = [], 0
+        for count in (nk, nk, n_experts, n_experts + 1, nk, nk, 1, 1):
+            at.append(end)
+            end += (count + 3) & ~3      # 16-byte aligned parts
+        out._at = at
+        out._buffer = torch.empty(end, dtype=torch.int32, device=device)
+        return out
+
+    def _tensor(self, i: int) -> torch.Tensor:
+        t = self._tensors[i]
+        if t is None:
+            n, e, k = self._sizes
+            shape = ((n, k), (n, k), (e,), (e + 1,), (n, k), (n * k,), (1,), (1,))[i]
+            size = shape[0] * shape[1] if len(shape) == 2 else shape[0]
+            t = self._buffer[self._at[i]:self._at[i] + size].view(shape)
+            if i in (1, 6):
+                t = t.view(torch.float32)
+            self._tensors[i] = t
+        return t
+
+    ids = property(lambda self: self._tensor(0))
+    w = property(lambda self: self._tensor(1))
+    counts = property(lambda self: self._tensor(2))
+    offsets = property(lambda self: self._tensor(3))
+    pos = property(lambda self: self._tensor(4))
+    order = property(lambda self: self._tensor(5))
+    loss = property(lambda self: self._tensor(6))
+    n_live = property(lambda self: self._tensor(7))
+
+    @property
+    def top_k(self) -> int:
+        return self._tensors[0].shape[1] if self._buffer is None else self._sizes[2]
+
+    def _operands(self, index: int, n: int, e: int, k: int):
+        """The eight addresses in the order of NAMES, checked."""
+        buffer = self._buffer
+        if buffer is not None:  # made by empty(): only its device and sizes are in question
+            if self._sizes != (n, e, k):
+                raise ValueError(f"route has the shape (tokens, experts, top_k) = {self._sizes}, not {(n, e, k)}")
+            if buffer.get_device() != index:
+                raise ValueError(f"route is on {buffer.device}, the logits on cuda:{index}")
+            base = buffer.data_ptr()
+            return [base + 4 * at for at in self._at]
+        i32, f32, nk = torch.int32, torch.float32, (n, k)
+        return [_operand(t, name, index, dtype, shape) for t, name, dtype, shape in zip(
+            self._tensors, MoeRoute.NAMES, (i32, f32, i32, i32, i32, i32, f32, i32),
+            (nk, nk, (e,), (e + 1,), nk, (n * k,), (1,), (1,)))]
 
 
 def moe_route_workspace(n_tokens: int, n_experts: int, top_k: int, device) -> torch.Tensor:
@@ -698,14 +744,8 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, renorm: bool = True, mask: O
     out.renorm = bool(renorm)
     if workspace is None:
         workspace = _allocate(stream, moe_route_workspace, n, e, top_k, logits.device)
-    i32, f32, nk = torch.int32, torch.float32, (n, top_k)
     _launch("moe_route_fwd", index, stream, x, m, n, e, top_k, int(out.renorm), _dtype_code(logits),
-            _operand(out.ids, "ids", index, i32, nk), _operand(out.w, "w", index, f32, nk),
-            _operand(out.counts, "counts", index, i32, (e,)),
-            _operand(out.offsets, "offsets", index, i32, (e + 1,)),
-            _operand(out.pos, "pos", index, i32, nk), _operand(out.order, "order", index, i32, (n * top_k,)),
-            _operand(out.loss, "loss", index, f32, (1,)), _operand(out.n_live, "n_live", index, i32, (1,)),
-            _scratch(workspace, index), workspace.numel())
+            *out._operands(index, n, e, top_k), _scratch(workspace, index), workspace.numel())
     return out
 
 
@@ -715,17 +755,14 @@ def moe_route_bwd(logits: torch.Tensor, route: MoeRoute, dloss: Optional[torch.T
     """dlogits from the gradients of the balance loss (fp32 [1]) and of the
     weights (fp32 [N][k]); logits and mask as in the forward that gave route."""
     index, n, e, x, m = _logits_operands(logits, mask)
-    k = route.ids.shape[1]
+    k = route.top_k
     if out is None:
         out = _allocate(stream, torch.empty_like, logits)
-    i32, f32 = torch.int32, torch.float32
-    _launch("moe_route_bwd", index, stream, x, m, n, e, k, int(route.renorm), _dtype_code(logits),
-            _operand(route.ids, "ids", index, i32, (n, k)), _operand(route.w, "w", index, f32, (n, k)),
-            _operand(route.counts, "counts", index, i32, (e,)),
-            _operand(route.offsets, "offsets", index, i32, (e + 1,)),
-            _operand(route.n_live, "n_live", index, i32, (1,)),
-            None if dloss is None else _operand(dloss, "dloss", index, f32, (1,)),
-            None if dw is None else _operand(dw, "dw", index, f32, (n, k)),
+    ids, w, counts, offsets, _, _, _, n_live = route._operands(index, n, e, k)
+    _launch("moe_route_bwd", index, stream, x, m, n, e, k, int(route.renorm), _dtype_code(logits), ids, w, counts,
+            offsets, n_live,
+            None if dloss is None else _operand(dloss, "dloss", index, torch.float32, (1,)),
+            None if dw is None else _operand(dw, "dw", index, torch.float32, (n, k)),
             _operand(out, "out", index, logits.dtype, (n, e)))
     return out
 

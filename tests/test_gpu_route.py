@@ -243,3 +243,25 @@ def test_route_refusals(cuda_device):
         sge.moe_route_bwd(logits[:4], r)
     with pytest.raises(ValueError, match="dw"):
         sge.moe_route_bwd(logits, r, dw=torch.zeros(8, 3, device=cuda_device))
+
+
+def test_route_of_the_callers_own_tensors(cuda_device):
+    """A MoeRoute of separate tensors gets the same results as one of
+    MoeRoute.empty, and is checked tensor by tensor."""
+    n, e, k = 37, 11, 3
+    logits = torch.randn(n, e, device=cuda_device)
+    want = sge.moe_route_fwd(logits, k)
+    i = lambda *s: torch.full(s, 7, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    f = lambda *s: torch.full(s, 7.0, device=cuda_device)  # noqa: E731
+    own = sge.MoeRoute(i(n, k), f(n, k), i(e), i(e + 1), i(n, k), i(n * k), f(1), i(1))
+    got = sge.moe_route_fwd(logits, k, out=own)
+    assert got is own
+    for name in sge.MoeRoute.NAMES:
+        assert torch.equal(getattr(got, name), getattr(want, name)), name
+    dw, one = torch.randn(n, k, device=cuda_device), torch.ones(1, device=cuda_device)
+    assert torch.equal(sge.moe_route_bwd(logits, own, one, dw), sge.moe_route_bwd(logits, want, one, dw))
+    bad = sge.MoeRoute(i(n, k), f(n, k), i(e), i(e), i(n, k), i(n * k), f(1), i(1))
+    with pytest.raises(ValueError, match="offsets"):
+        sge.moe_route_fwd(logits, k, out=bad)
+    with pytest.raises(ValueError, match="shape"):
+        sge.moe_route_fwd(logits, k + 1, out=want)

@@ -359,3 +359,21 @@ def test_int8_ffn_rejects_bad_arguments(lib, routed):
     need = lib.int8_ffn_workspace_bytes(10, 64, 128, 4, 2, sge.SGE_BF16)
     assert need > 0 and need % 256 == 0
     assert lib.int8_ffn_workspace_bytes(10, 60, 128, 4, 2, sge.SGE_BF16) == 0
+
+
+def test_binding_of_the_8_bit_operators_and_the_router_refuses_cpu_tensors():
+    import torch
+    x = torch.zeros(4, 64)
+    rows = sge.Int8Rows.empty(4, 64, "cpu")
+    assert rows.q.shape == (4, 64) and rows.scale.shape == (4,) and rows.rows == 4
+    route = sge.MoeRoute.empty(4, 8, 2, "cpu")
+    assert route.ids.shape == route.w.shape == route.pos.shape == (4, 2) and route.w.dtype == torch.float32
+    assert route.offsets.shape == (9,) and route.order.shape == (8,) and route.top_k == 2
+    ends = [getattr(route, a).data_ptr() for a in sge.MoeRoute.NAMES]
+    assert all(p % 4 == 0 for p in ends) and len(set(ends)) == 8
+    for call in (lambda: sge.int8_quant_rows(x), lambda: sge.int8_linear(rows, rows),
+                 lambda: sge.twell_gate_pack_int8(rows, rows, 16, 16), lambda: sge.moe_route_fwd(x, 2),
+                 lambda: sge.moe_route_bwd(x[:, :8], route), lambda: sge.int8_ffn_fwd(x, rows, rows, rows),
+                 lambda: sge.moe_int8_ffn_fwd(x, rows, rows, rows, route.w, route.offsets, route.pos)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()

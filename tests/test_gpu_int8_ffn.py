@@ -119,7 +119,7 @@ def run_experts(cuda_device, n, d, f, e, k, dtype, ids=None, seed=0, x=None):
                                        (4, 1024, 256, 32, 4), (17, 64, 136, 3, 2), (100, 256, 256, 8, 2),
                                        (300, 128, 384, 4, 2), (500, 264, 264, 256, 3), (1200, 128, 256, 3, 1),
                                        (700, 256, 520, 2, 2), (1300, 1544, 264, 2, 2), (2, 136, 264, 1, 1),
-                                       (8, 64, 264, 16, 4), (7, 72, 136, 100, 16)])
+                                       (8, 64, 264, 16, 4), (7, 72, 136, 100, 16), (50, 64, 136, 1, 1)])
 def test_experts(cuda_device, dtype, n, d, f, e, k):
     y, want, mag, parts = run_experts(cuda_device, n, d, f, e, k, dtype)
     assert_close(y, want, mag, f, dtype, parts)

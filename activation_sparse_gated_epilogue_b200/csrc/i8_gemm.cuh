@@ -42,6 +42,9 @@ struct I8Shape {
   // from it to the epilogue (setmaxnreg works on whole warpgroups)
   static constexpr bool MOVE_REGS = PER_BLOCK && HALVES == 2 && BN / HALVES > 64;
   static constexpr int FIRST_EPI = MOVE_REGS ? 4 : 2;
+  // what the warpgroups ask for with setmaxnreg: it draws on the registers of
+  // the launch, so their sum may not pass those (launch_i8_gemm checks it)
+  static constexpr int FEW_REGS = 56, MANY_REGS = 224;
   static constexpr int THREADS = 32 * FIRST_EPI + 128 * HALVES;
   static constexpr int BM = PAIR ? 2 * kBM : kBM;
   // B rows of one load.  NB = 2: two matrices' tiles of BN rows side by side
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
   // MOVE_REGS: 384 threads start with 168 registers each (64,512 in all); 56 for
   // the first warpgroup and 224 for the two epilogue warpgroups are as many
   if (warp < Shape::FIRST_EPI) {
-    if constexpr (Shape::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (Shape::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::FEW_REGS));
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer
       int s = 0;
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
     __syncwarp();
   } else {
     // --------------------------------------------------------- epilogue
-    if constexpr (Shape::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (Shape::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::MANY_REGS));
     const int quarter = warp & 3;      // TMEM lanes this warp may access
     const int half = (warp - Shape::FIRST_EPI) >> 2;  // column half (HALVES = 2)
     constexpr int COLS = BN / Shape::HALVES;
@@ -614,6 +617,15 @@ int launch_i8_gemm(const I8Maps& m, const I8Problem& p, const Epi& epi, int32_t*
   int rc = set_smem_limit(reinterpret_cast<const void*>(kern), Shape::SMEM_BYTES);
   if (rc) return rc;
   // the most row blocks there can be: with groups, one partial block more for each
+  if constexpr (Shape::MOVE_REGS) {
+    static const int launch_regs = [&] {
+      cudaFuncAttributes attr = {};
+      return cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(kern)) == cudaSuccess ? attr.numRegs : 0;
+    }();
+    if (launch_regs * Shape::THREADS < 128 * Shape::FEW_REGS + 256 * Shape::MANY_REGS)
+      return fail(SGE_ERR_CUDA, "%s: built with %d registers a thread, too few for its warpgroups' shares", what,
+                  launch_regs);
+  }
   int64_t m_blocks = (p.rows + Shape::BM - 1) / Shape::BM;
   if (p.offsets) m_blocks += p.groups - 1 < p.rows ? p.groups - 1 : p.rows;
   const int64_t tiles = m_blocks * ((p.n + Shape::BN - 1) / Shape::BN) * p.splits;

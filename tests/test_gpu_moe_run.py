@@ -126,10 +126,10 @@ def test_debug_build_gives_the_same_bits_and_flags_bad_plans(cuda_device):
     path = sge_build.LIB_DEBUG
     assert os.path.exists(path)
     rng = np.random.default_rng(8)
-    d, f, e, k = 128, 264, 5, 2
+    d, f, e, k = 1024, 264, 5, 2
     ex = Experts(rng, e, d, f, cuda_device)
     one = torch.ones(1, device=cuda_device)
-    for n in (3, 40, 3000):
+    for n in (3, 40, 3000):            # few tokens, single CTAs, CTA pairs
         x = tokens(rng, n, d, torch.float32).to(cuda_device)
         logits = torch.randn(n, e, device=cuda_device)
         dw = torch.randn(n, k, device=cuda_device)

@@ -3,6 +3,8 @@ as a serving loop and as a training step use them; two calls at once; the
 debug build; the bounded waits of the 8-bit engine."""
 import ctypes
 import os
+import subprocess
+import sys
 import time
 
 import numpy as np
@@ -120,6 +122,36 @@ def test_two_calls_at_once(cuda_device):
         got.append([call(*m, stream=s) for m, s in zip(made, streams)])
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for pair in got for a, b in zip(pair, want))
+
+
+def test_first_calls_of_a_process_in_a_capture(cuda_device):
+    """Nothing that a first call sets up (limits, attributes, occupancy) breaks
+    the capture of a graph: a fresh process captures before it calls anything."""
+    code = """
+import torch
+import activation_sparse_gated_epilogue_b200 as sge
+def rows(r, c):
+    return sge.Int8Rows(torch.randint(-127, 128, (r, c), dtype=torch.int8, device="cuda"),
+                        torch.rand(r, device="cuda") * 0.01, c)
+x, logits = torch.randn(3000, 1024, device="cuda"), torch.randn(3000, 64, device="cuda")
+w, block = rows(512, 1024), [rows(512, 1024), rows(512, 1024), rows(1024, 512)]
+def run():
+    r = sge.moe_route_fwd(logits, 4)
+    q = sge.int8_quant_rows(x)
+    tw = sge.twell_gate_pack_int8(q, w, 128, 128)
+    return [sge.int8_linear(q, w, torch.float32), sge.int8_ffn_fwd(x, *block), r.order, tw.count,
+            sge.moe_route_bwd(logits, r, torch.ones_like(r.loss))]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_debug_build_gives_the_same_bits_and_flags_bad_plans(cuda_device):

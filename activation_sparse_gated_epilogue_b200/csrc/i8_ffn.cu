@@ -170,20 +170,22 @@ struct EpiI8Down {
 };
 
 // y[t] = sum over the token's places of w * (sum over splits of z), in the
-// order of the token's experts and of the splits.  Z: the type z is kept in.
-// Whole sums (one split) are kept in the activations' type, which rounds a
-// bf16 result once per expert and once in the end: half the bytes of fp32.
+// order of the token's experts and of the splits.  z is kept in fp32 whatever
+// the activations' type, so that y is rounded once, in the end, on every path:
+// with z in bf16 a token's result was less exact (0.0023 against 0.0017 of its
+// norm) in the batches whose down product is not split than in the others.
 // One warp per token and 256 U columns, U vectors of 8 a lane; loads are
 // clamped, not branched around, so that those of a place and of several splits
-// are in flight together (8000 tokens of 2048 features, two places each: 22 us
-// from HBM; 36 us with a branch before each vector).
-template <class T, class Z, int U>
+// are in flight together (with a branch before each vector it took 1.6 times as
+// long).  8000 tokens over 16 experts of 2048 x 2048, two a token: the block took
+// 238 us with z in bf16 and takes 257 us (131 MB more through HBM).
+template <class T, int U>
 __global__ void __launch_bounds__(256, 4)
-    i8_combine_kernel(const Z* __restrict__ z, int rows, int splits, int64_t n, int d, int k,
+    i8_combine_kernel(const float* __restrict__ z, int rows, int splits, int64_t n, int d, int k,
                       const float* __restrict__ w, const int32_t* __restrict__ pos, T* __restrict__ y) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int W = 8, N = Vec16<Z>::N;
+  constexpr int W = 8, N = Vec16<float>::N;
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (t >= n) return;
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(256, 4)
     const uint32_t p = __shfl_sync(0xffffffffu, my_place, a);
     const float wt = __shfl_sync(0xffffffffu, my_w, a);
     if (p >= static_cast<uint32_t>(rows)) continue;
-    const Z* src = z + static_cast<int64_t>(p) * d;
+    const float* src = z + static_cast<int64_t>(p) * d;
     float part[U][W];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(256, 4)
 #pragma unroll
         for (int j = 0; j < W / N; ++j) {
           float f[N];
-          Vec16<Z>::unpack(raw[u][j], f);
+          Vec16<float>::unpack(raw[u][j], f);
 #pragma unroll
           for (int m = 0; m < N; ++m) part[u][j * N + m] += f[m];
         }
@@ -250,8 +252,7 @@ struct FfnPlan {
   bool small;       // the kernels for a few tokens
   bool pairs;       // CTA-pair tiles
   int splits;       // parts of the down projection's K
-  bool combine;     // y is summed from z by the combine kernel
-  bool z_f32;
+  bool combine;     // y is summed from z (fp32) by the combine kernel
   int64_t ldx, ldh;
   size_t xq, sx, hq, hs, z, total;  // workspace offsets
 };
@@ -261,7 +262,7 @@ using GateUpOne = I8Shape<128, 2, 2, 1, false, true, false, 0>;
 using DownPair = I8Shape<256, 1, 2, 2, true, true, true, 4096>;
 using DownOne = I8Shape<128, 1, 4, 2, false, true, true, 4096>;
 
-static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype, bool routed) {
+static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, bool routed) {
   FfnPlan p = {};
   p.rows = routed ? n * k : n;
   // A few tokens whose quantised rows fit a block's shared memory, at most two
@@ -290,7 +291,6 @@ static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype
     p.splits = static_cast<int>((kb + per - 1) / per);
   }
   p.combine = !p.small && (routed || p.splits > 1);
-  p.z_f32 = p.splits > 1 || dtype == SGE_F32;
   p.ldx = round16(d);
   p.ldh = round16(f);
   size_t at = 0;
@@ -303,7 +303,7 @@ static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, int dtype
   p.sx = take(static_cast<size_t>(p.rows) * 4);
   p.hq = take(static_cast<size_t>(p.rows) * p.ldh);
   p.hs = take(static_cast<size_t>(p.rows) * kb * 4);
-  p.z = p.combine ? take(static_cast<size_t>(p.rows) * p.splits * d * (p.z_f32 ? 4 : 2)) : 0;
+  p.z = p.combine ? take(static_cast<size_t>(p.rows) * p.splits * d * 4) : 0;
   p.total = at;
   return p;
 }
@@ -341,14 +341,14 @@ static int ffn_gate_up(const FfnArgs& a, const FfnPlan& p, const I8Problem& pr) 
   return launch_i8_gemm<Shape>(m, pr, epi, a.diag, a.st, "int8 ffn (gate, up)");
 }
 
-template <class T, class Z>
+template <class T>
 static int ffn_combine(const FfnArgs& a, const FfnPlan& p) {
   // one vector a lane while the warps of two still fit the GPU at once
   const int u = a.n * ((a.d + 255) / 256) <= 148 * 32 ? 1 : 2;
-  auto kern = u == 1 ? i8_combine_kernel<T, Z, 1> : i8_combine_kernel<T, Z, 2>;
+  auto kern = u == 1 ? i8_combine_kernel<T, 1> : i8_combine_kernel<T, 2>;
   const dim3 grid(static_cast<unsigned>((a.n + 7) / 8), static_cast<unsigned>((a.d + 256 * u - 1) / (256 * u)));
   return launch_pdl(kern, grid, dim3(256), 0, a.st,
-                    "int8 ffn (combine)", reinterpret_cast<const Z*>(a.ws + p.z), static_cast<int>(p.rows), p.splits,
+                    "int8 ffn (combine)", reinterpret_cast<const float*>(a.ws + p.z), static_cast<int>(p.rows), p.splits,
                     a.n, static_cast<int>(a.d), a.k, a.w, a.pos, static_cast<T*>(a.y));
 }
 
@@ -386,14 +386,9 @@ static int ffn(const FfnArgs& a, const FfnPlan& p) {
     T* y = static_cast<T*>(a.y);
     return p.pairs ? ffn_down<DownPair>(a, p, down, y) : ffn_down<DownOne>(a, p, down, y);
   }
-  if (p.z_f32) {
-    float* z = reinterpret_cast<float*>(a.ws + p.z);
-    rc = p.pairs ? ffn_down<DownPair>(a, p, down, z) : ffn_down<DownOne>(a, p, down, z);
-    return rc ? rc : ffn_combine<T, float>(a, p);
-  }
-  T* z = reinterpret_cast<T*>(a.ws + p.z);
+  float* z = reinterpret_cast<float*>(a.ws + p.z);
   rc = p.pairs ? ffn_down<DownPair>(a, p, down, z) : ffn_down<DownOne>(a, p, down, z);
-  return rc ? rc : ffn_combine<T, T>(a, p);
+  return rc ? rc : ffn_combine<T>(a, p);
 }
 
 static int check_ffn_sizes(const char* fn, int64_t n, int64_t d, int64_t f, int e, int k, int dtype) {
@@ -420,7 +415,7 @@ static int run_ffn(const char* fn, FfnArgs a, int dtype, bool routed, void* work
       !aligned16(a.wd) || !aligned16(a.sd) || !aligned16(a.y) || !aligned16(a.w) || !aligned16(a.offsets) ||
       !aligned16(a.pos) || !aligned16(a.diag) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(SGE_ERR_ARG, "%s: pointer not 16-byte aligned (workspace: 256)", fn);
-  const FfnPlan p = ffn_plan(a.n, a.d, a.f, a.e, a.k, dtype, routed);
+  const FfnPlan p = ffn_plan(a.n, a.d, a.f, a.e, a.k, routed);
   if (workspace_bytes < p.total)
     return fail(SGE_ERR_ARG, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, p.total);
   a.ws = static_cast<uint8_t*>(workspace);
@@ -435,8 +430,8 @@ extern "C" size_t int8_ffn_workspace_bytes(int64_t n_tokens, int64_t d_model, in
                                            int dtype) {
   if (check_ffn_sizes("int8_ffn_workspace_bytes", n_tokens, d_model, d_ff, n_experts, top_k, dtype)) return 0;
   // int8_ffn_fwd and moe_int8_ffn_fwd both take it
-  const size_t routed = ffn_plan(n_tokens, d_model, d_ff, n_experts, top_k, dtype, true).total;
-  const size_t dense = ffn_plan(n_tokens, d_model, d_ff, n_experts, top_k, dtype, false).total;
+  const size_t routed = ffn_plan(n_tokens, d_model, d_ff, n_experts, top_k, true).total;
+  const size_t dense = ffn_plan(n_tokens, d_model, d_ff, n_experts, top_k, false).total;
   return n_experts > 1 || routed > dense ? routed : dense;
 }
 

@@ -555,8 +555,7 @@ int moe_route_bwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int
  *   moe_route_fwd.  A place of -1 adds nothing; a token without places gets
  *   y = 0.  Places and bounds outside [0, N * top_k] are left out, never
  *   followed.  Each expert's weights are read only if it has tokens.
- *   With SGE_BF16 an expert's y may be rounded to bf16 before the weighted sum
- *   (one rounding per expert and one of the sum).
+ *   The experts' results and their weighted sum are fp32; y is rounded once.
  *
  * Results do not depend on scheduling.  The workspace (256-byte aligned,
  * int8_ffn_workspace_bytes for either call; n_experts = top_k = 1 for

@@ -225,3 +225,13 @@ def test_refusals(cuda_device):
     with pytest.raises(ValueError, match="CUDA"):
         sge.int8_ffn_fwd(x.cpu(), *one.dev)
     assert sge.int8_ffn_fwd(x[:0], *one.dev).shape == (0, 64)
+
+
+@pytest.mark.parametrize("n,d,f,e,k", [(300, 128, 384, 4, 2), (700, 256, 520, 2, 2), (1300, 1544, 264, 2, 2),
+                                       (1200, 128, 256, 3, 1), (50, 64, 136, 1, 1), (4, 1024, 256, 32, 4),
+                                       (40, 128, 2056, 4, 2), (300, 128, 384, 16, 8)])
+def test_experts_results_are_rounded_once(cuda_device, n, d, f, e, k):
+    """A bf16 y is the rounding of an fp32 sum over the experts on every path:
+    whole and split down products, single CTAs and pairs, few tokens."""
+    y, want, mag, _ = run_experts(cuda_device, n, d, f, e, k, torch.bfloat16)
+    assert_close(y, want, mag, f, torch.bfloat16)

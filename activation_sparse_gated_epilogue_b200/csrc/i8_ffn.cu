@@ -174,13 +174,15 @@ struct EpiI8Down {
 // the activations' type, so that y is rounded once, in the end, on every path:
 // with z in bf16 a token's result was less exact (0.0023 against 0.0017 of its
 // norm) in the batches whose down product is not split than in the others.
-// One warp per token and 256 U columns, U vectors of 8 a lane; loads are
-// clamped, not branched around, so that those of a place and of several splits
-// are in flight together (with a branch before each vector it took 1.6 times as
-// long).  8000 tokens over 16 experts of 2048 x 2048, two a token: the block took
-// 238 us with z in bf16 and takes 257 us (131 MB more through HBM).
-template <class T, int U>
-__global__ void __launch_bounds__(256, 4)
+// One warp per token and 256 columns, eight a lane; columns are clamped, not
+// branched around, so that the loads of several splits and places are in flight
+// together (with a branch before each it took 1.6 times as long).  8000 tokens
+// over 16 experts of 2048 x 2048, two a token: the block took 238 us with z in
+// bf16 and takes 257 us (131 MB more through HBM).  Sixteen columns a lane spill
+// at four blocks per SM (64 registers): 1-3% more of the block at 2048 to 12000
+// tokens over 8 to 32 experts.
+template <class T>
+__global__ void __launch_bounds__(256, 6)
     i8_combine_kernel(const float* __restrict__ z, int rows, int splits, int64_t n, int d, int k,
                       const float* __restrict__ w, const int32_t* __restrict__ pos, T* __restrict__ y) {
   grid_dep_wait();
@@ -195,52 +197,37 @@ __global__ void __launch_bounds__(256, 4)
     my_place = pos ? checked_place(pos[t * k + lane], rows) : static_cast<uint32_t>(t);
     if (w) my_w = w[t * k + lane];
   }
-  int col[U];
+  const int col = (blockIdx.y * 32 + lane) * W, from = min(col, d - W);  // d % 8 == 0
+  float sum[W];
 #pragma unroll
-  for (int u = 0; u < U; ++u) col[u] = ((blockIdx.y * U + u) * 32 + lane) * W;  // d % 8 == 0
-  float sum[U][W];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int j = 0; j < W; ++j) sum[u][j] = 0.0f;
+  for (int j = 0; j < W; ++j) sum[j] = 0.0f;
   const int64_t split_step = static_cast<int64_t>(rows) * d;
 #pragma unroll 2
   for (int a = 0; a < k; ++a) {
     const uint32_t p = __shfl_sync(0xffffffffu, my_place, a);
     const float wt = __shfl_sync(0xffffffffu, my_w, a);
     if (p >= static_cast<uint32_t>(rows)) continue;
-    const float* src = z + static_cast<int64_t>(p) * d;
-    float part[U][W];
+    const float* src = z + static_cast<int64_t>(p) * d + from;
+    float part[W];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < W; ++j) part[u][j] = 0.0f;
+    for (int j = 0; j < W; ++j) part[j] = 0.0f;
 #pragma unroll 2
     for (int s = 0; s < splits; ++s) {
-      uint4 raw[U][W / N];
+      uint4 raw[W / N];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int j = 0; j < W / N; ++j) raw[j] = *reinterpret_cast<const uint4*>(src + s * split_step + j * N);
 #pragma unroll
-        for (int j = 0; j < W / N; ++j)
-          raw[u][j] = *reinterpret_cast<const uint4*>(src + s * split_step + min(col[u], d - W) + j * N);
+      for (int j = 0; j < W / N; ++j) {
+        float f[N];
+        Vec16<float>::unpack(raw[j], f);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < W / N; ++j) {
-          float f[N];
-          Vec16<float>::unpack(raw[u][j], f);
-#pragma unroll
-          for (int m = 0; m < N; ++m) part[u][j * N + m] += f[m];
-        }
+        for (int m = 0; m < N; ++m) part[j * N + m] += f[m];
+      }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < W; ++j) sum[u][j] = fmaf(wt, part[u][j], sum[u][j]);
+    for (int j = 0; j < W; ++j) sum[j] = fmaf(wt, part[j], sum[j]);
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (col[u] < d) store8(y + t * d + col[u], sum[u]);
+  if (col < d) store8(y + t * d + col, sum);
 }
 
 // ------------------------------------------------------------------- host
@@ -343,13 +330,10 @@ static int ffn_gate_up(const FfnArgs& a, const FfnPlan& p, const I8Problem& pr) 
 
 template <class T>
 static int ffn_combine(const FfnArgs& a, const FfnPlan& p) {
-  // one vector a lane while the warps of two still fit the GPU at once
-  const int u = a.n * ((a.d + 255) / 256) <= 148 * 32 ? 1 : 2;
-  auto kern = u == 1 ? i8_combine_kernel<T, 1> : i8_combine_kernel<T, 2>;
-  const dim3 grid(static_cast<unsigned>((a.n + 7) / 8), static_cast<unsigned>((a.d + 256 * u - 1) / (256 * u)));
-  return launch_pdl(kern, grid, dim3(256), 0, a.st,
-                    "int8 ffn (combine)", reinterpret_cast<const float*>(a.ws + p.z), static_cast<int>(p.rows), p.splits,
-                    a.n, static_cast<int>(a.d), a.k, a.w, a.pos, static_cast<T*>(a.y));
+  const dim3 grid(static_cast<unsigned>((a.n + 7) / 8), static_cast<unsigned>((a.d + 255) / 256));
+  return launch_pdl(i8_combine_kernel<T>, grid, dim3(256), 0, a.st, "int8 ffn (combine)",
+                    reinterpret_cast<const float*>(a.ws + p.z), static_cast<int>(p.rows), p.splits, a.n,
+                    static_cast<int>(a.d), a.k, a.w, a.pos, static_cast<T*>(a.y));
 }
 
 template <class T>

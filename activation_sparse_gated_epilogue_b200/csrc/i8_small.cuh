@@ -105,32 +105,64 @@ struct SmallFfn {
 
 constexpr int kSmallRows = kSmallTokens * 16;  // places of at most kSmallTokens tokens
 
-// Rows [*lo, *hi) of expert e, clamped like the tile engine's bounds.
-SGE_DEV void small_rows(const SmallFfn& a, int e, int rows, int* lo, int* hi) {
-  *lo = a.offsets ? checked_bound(a.offsets[e], 0, rows) : 0;
-  *hi = a.offsets ? checked_bound(a.offsets[e + 1], *lo, rows) : rows;
-}
-
-// The experts that have rows, in order (any block size; experts <= 256).
-// Returns their number.  list: experts ints; scratch: 8 ints.
-SGE_DEV int used_experts(const SmallFfn& a, int rows, int* list, int* scratch) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  bool used = false;
-  if (threadIdx.x < a.experts) {
-    int lo, hi;
-    small_rows(a, threadIdx.x, rows, &lo, &hi);
-    used = hi > lo;
+// The experts' row bounds, as the tile engine makes them (out of range or out of
+// order they give fewer rows, never an overlap), and the experts that have rows,
+// in order (any block size; experts <= 256, rows <= 128): expert e has the rows
+// [bounds[e], bounds[e + 1]), so at most min(experts, rows) have any.  Returns
+// their number.  list: experts bytes; bounds: experts + 1 bytes; scratch: 8 ints.
+SGE_DEV int used_experts(const SmallFfn& a, int rows, uint8_t* list, uint8_t* bounds, int* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = threadIdx.x;
+  int lo = 0, hi = 0;
+  if (e < a.experts) {
+    lo = a.offsets ? checked_bound(a.offsets[e], 0, rows) : 0;
+    hi = a.offsets ? checked_bound(a.offsets[e + 1], 0, rows) : rows;
+    bounds[e] = static_cast<uint8_t>(lo);
+    if (e == a.experts - 1) bounds[a.experts] = static_cast<uint8_t>(hi);
   }
-  const uint32_t mask = __ballot_sync(0xffffffffu, used);
-  if (lane == 0 && warp < 8) scratch[warp] = __popc(mask);
+  // scratch[w]: warp w's used experts, and a high bit if its bounds descend
+  // somewhere (a route's do not: a scan for everyone took 0.5 us of each kernel's 10)
+  constexpr int DESCENDS = 1 << 16;
+  uint32_t mask = __ballot_sync(0xffffffffu, hi > lo);
+  const uint32_t down = __ballot_sync(0xffffffffu, hi < lo);
+  if (lane == 0 && warp < 8) scratch[warp] = __popc(mask) | (down ? DESCENDS : 0);
   __syncthreads();
-  int before = 0, all = 0;
+  const auto count = [&](int& before) {
+    int all = 0;
+    before = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    if (w < warp) before += scratch[w];
-    all += scratch[w];
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += scratch[w];
+      all += scratch[w];
+    }
+    return all;
+  };
+  int before, all = count(before);
+  if (all >= DESCENDS) {
+    __syncthreads();
+    if (warp == 0) {  // each bound becomes the largest up to it
+      int top = 0;
+      for (int i0 = 0; i0 <= a.experts; i0 += 32) {
+        int v = i0 + lane <= a.experts ? max(static_cast<int>(bounds[i0 + lane]), top) : top;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v = max(v, u);
+        }
+        if (i0 + lane <= a.experts) bounds[i0 + lane] = static_cast<uint8_t>(v);
+        top = __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
+    if (e < a.experts) {
+      lo = bounds[e];
+      hi = bounds[e + 1];
+    }
+    mask = __ballot_sync(0xffffffffu, hi > lo);
+    if (lane == 0 && warp < 8) scratch[warp] = __popc(mask);
+    __syncthreads();
+    all = count(before);
   }
-  if (used) list[before + __popc(mask & ((1u << lane) - 1u))] = threadIdx.x;
+  if (hi > lo) list[before + __popc(mask & ((1u << lane) - 1u))] = static_cast<uint8_t>(e);
   __syncthreads();
   return all;
 }
@@ -145,18 +177,18 @@ __global__ void __launch_bounds__(512, 1) i8_small_up_kernel(const T* __restrict
   extern __shared__ __align__(16) int8_t s_x[];  // [NT][ldx]
   __shared__ __align__(16) float s_h[NT][kHGroup];  // read in 16-byte pieces
   __shared__ float s_scale[NT];
-  __shared__ int s_list[kMaxGroups], s_scratch[8], s_token[kSmallRows];
+  __shared__ int s_scratch[8], s_token[kSmallRows];
+  __shared__ uint8_t s_list[kMaxGroups], s_bounds[kMaxGroups + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = static_cast<int>(a.n) * a.k;
   const int group = blockIdx.x, u0 = group * kHGroup;
   grid_dep_wait();
   grid_dep_launch();
   for (int i = threadIdx.x; i < rows; i += 512) s_token[i] = a.pos ? -1 : i;
-  const int used = used_experts(a, rows, s_list, s_scratch);
+  const int used = used_experts(a, rows, s_list, s_bounds, s_scratch);
   if (blockIdx.y >= used) return;
   const int e = s_list[blockIdx.y];
-  int lo, hi;
-  small_rows(a, e, rows, &lo, &hi);
+  const int lo = s_bounds[e], hi = s_bounds[e + 1];
   if (a.pos) {
     for (int i = threadIdx.x; i < rows; i += 512) {
       const uint32_t p = checked_place(a.pos[i], rows);
@@ -261,7 +293,8 @@ constexpr int kDownChannels = 4, kDownSlices = 4, kDownPiece = 2048;
 template <class T>
 __global__ void __launch_bounds__(512) i8_small_down_kernel(const SmallFfn a, T* __restrict__ y) {
   __shared__ float s_sum[kDownSlices][kDownChannels][kSmallTokens];
-  __shared__ int s_list[kMaxGroups], s_scratch[8], s_token[kSmallRows];
+  __shared__ int s_scratch[8], s_token[kSmallRows];
+  __shared__ uint8_t s_list[kMaxGroups], s_bounds[kMaxGroups + 1];
   __shared__ float s_w[kSmallRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ch = warp % kDownChannels, slice = warp / kDownChannels;
@@ -274,7 +307,7 @@ __global__ void __launch_bounds__(512) i8_small_down_kernel(const SmallFfn a, T*
     s_token[i] = a.pos ? -1 : i;
     s_w[i] = a.pos ? 0.0f : 1.0f;
   }
-  const int used = used_experts(a, rows, s_list, s_scratch);
+  const int used = used_experts(a, rows, s_list, s_bounds, s_scratch);
   if (a.pos) {
     for (int i = threadIdx.x; i < rows; i += 512) {
       const uint32_t p = checked_place(a.pos[i], rows);
@@ -295,8 +328,7 @@ __global__ void __launch_bounds__(512) i8_small_down_kernel(const SmallFfn a, T*
       for (int i = 0; i < 4; ++i)
         v[i] = b0 + 512 * i < a.f ? load_weights(row + b0 + 512 * i) : make_uint4(0, 0, 0, 0);
       const float sd = __ldg(a.sd + static_cast<int64_t>(e) * a.d + c);
-      int lo, hi;
-      small_rows(a, e, rows, &lo, &hi);
+      const int lo = s_bounds[e], hi = s_bounds[e + 1];
       for (int r = lo; r < hi; ++r) {
         const int token = s_token[r];
         float part = 0.0f;

@@ -235,3 +235,41 @@ def test_experts_results_are_rounded_once(cuda_device, n, d, f, e, k):
     whole and split down products, single CTAs and pairs, few tokens."""
     y, want, mag, _ = run_experts(cuda_device, n, d, f, e, k, torch.bfloat16)
     assert_close(y, want, mag, f, torch.bfloat16)
+
+
+def guarded_call(ex, x, w, offsets, pos, fill):
+    """moe_int8_ffn_fwd with y and the workspace inside larger buffers, whose
+    other bytes must stay; the workspace is full of `fill` bytes."""
+    n, d, e = x.shape[0], x.shape[1], ex.e
+    need = sge.int8_ffn_workspace(n, d, ex.f, e, w.shape[1], x.dtype, x.device).numel()
+    ws = torch.full((need + 512,), fill, dtype=torch.uint8, device=x.device)
+    y = torch.full((n * d + 512,), 7.0, dtype=x.dtype, device=x.device)
+    sge.moe_int8_ffn_fwd(x, *ex.dev, w, offsets, pos, y=y[256:256 + n * d].view(n, d), workspace=ws[256:256 + need])
+    assert (ws[:256] == fill).all() and (ws[256 + need:] == fill).all()
+    assert (y[:256] == 7).all() and (y[256 + n * d:] == 7).all()
+    return y[256:256 + n * d].view(n, d).clone()
+
+
+def as_bounds(values, rows, device):
+    """Bounds as given, and the ascending ones that they stand for."""
+    made = np.maximum.accumulate(np.clip(np.array(values, np.int64), 0, rows))
+    return (torch.tensor(values, dtype=torch.int32, device=device),
+            torch.tensor(made.tolist(), dtype=torch.int32, device=device))
+
+
+@pytest.mark.parametrize("n,d", [(3, 64), (30, 64), (600, 64), (3000, 512)])
+def test_bounds_out_of_order_stand_for_ascending_ones(cuda_device, n, d):
+    """On every path (few tokens, single CTAs, pairs) an expert's rows begin
+    where those of the experts before it end."""
+    rng = np.random.default_rng(5)
+    f, e, k = 128, 3, 2
+    ex = Experts(rng, e, d, f, cuda_device)
+    x = tokens(rng, n, d, torch.float32).to(cuda_device)
+    r = sge.moe_route_fwd(torch.randn(n, e, device=cuda_device), k)
+    rows = n * k
+    for values in ([0, rows, 1, rows], [0, rows // 2, rows // 3, rows], [0, -5, rows, 7 * n],
+                   [0, 2 ** 31 - 1, -2 ** 31, 5], [0, 1, 0, rows]):
+        bad, good = as_bounds(values, rows, cuda_device)
+        want = guarded_call(ex, x, r.w, good, r.pos, 0)
+        for fill in (0, 255):
+            assert torch.equal(guarded_call(ex, x, r.w, bad, r.pos, fill), want), values

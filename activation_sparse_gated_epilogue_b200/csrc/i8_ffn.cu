@@ -178,19 +178,28 @@ struct EpiI8Down {
 // branched around, so that the loads of several splits and places are in flight
 // together (with a branch before each it took 1.6 times as long).  8000 tokens
 // over 16 experts of 2048 x 2048, two a token: the block took 238 us with z in
-// bf16 and takes 257 us (131 MB more through HBM).  Sixteen columns a lane spill
+// bf16 and takes 251 us (131 MB more through HBM).  Sixteen columns a lane spill
 // at four blocks per SM (64 registers): 1-3% more of the block at 2048 to 12000
 // tokens over 8 to 32 experts.
 template <class T>
 __global__ void __launch_bounds__(256, 6)
     i8_combine_kernel(const float* __restrict__ z, int rows, int splits, int64_t n, int d, int k,
-                      const float* __restrict__ w, const int32_t* __restrict__ pos, T* __restrict__ y) {
+                      const float* __restrict__ w, const int32_t* __restrict__ pos,
+                      const int32_t* __restrict__ offsets, int experts, T* __restrict__ y) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr int W = 8, N = Vec16<float>::N;
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (t >= n) return;
+  // the experts' rows, all together: only there has z been written
+  int begin = 0, end = rows;
+  if (offsets) {
+    begin = checked_bound(offsets[0], 0, rows);
+    end = 0;
+    for (int i = lane; i <= experts; i += 32) end = max(end, checked_bound(offsets[i], 0, rows));
+    end = __reduce_max_sync(0xffffffffu, end);
+  }
   uint32_t my_place = 0xffffffffu;
   float my_w = 1.0f;
   if (lane < k) {
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(256, 6)
   for (int a = 0; a < k; ++a) {
     const uint32_t p = __shfl_sync(0xffffffffu, my_place, a);
     const float wt = __shfl_sync(0xffffffffu, my_w, a);
-    if (p >= static_cast<uint32_t>(rows)) continue;
+    if (p < static_cast<uint32_t>(begin) || p >= static_cast<uint32_t>(end)) continue;
     const float* src = z + static_cast<int64_t>(p) * d + from;
     float part[W];
 #pragma unroll
@@ -333,7 +342,7 @@ static int ffn_combine(const FfnArgs& a, const FfnPlan& p) {
   const dim3 grid(static_cast<unsigned>((a.n + 7) / 8), static_cast<unsigned>((a.d + 255) / 256));
   return launch_pdl(i8_combine_kernel<T>, grid, dim3(256), 0, a.st, "int8 ffn (combine)",
                     reinterpret_cast<const float*>(a.ws + p.z), static_cast<int>(p.rows), p.splits, a.n,
-                    static_cast<int>(a.d), a.k, a.w, a.pos, static_cast<T*>(a.y));
+                    static_cast<int>(a.d), a.k, a.w, a.pos, a.offsets, a.e, static_cast<T*>(a.y));
 }
 
 template <class T>

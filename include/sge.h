@@ -554,7 +554,10 @@ int moe_route_bwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int
  *   w fp32 [N][top_k], offsets int32 [E + 1], pos int32 [N][top_k] as given by
  *   moe_route_fwd.  A place of -1 adds nothing; a token without places gets
  *   y = 0.  Places and bounds outside [0, N * top_k] are left out, never
- *   followed.  Each expert's weights are read only if it has tokens.
+ *   followed; bounds out of order stand for the ascending ones that begin where
+ *   those before them end; a place in no expert's rows adds nothing.  A place
+ *   that two assignments name has no defined value.  Each expert's weights are
+ *   read only if it has tokens.
  *   The experts' results and their weighted sum are fp32; y is rounded once.
  *
  * Results do not depend on scheduling.  The workspace (256-byte aligned,

@@ -273,3 +273,30 @@ def test_bounds_out_of_order_stand_for_ascending_ones(cuda_device, n, d):
         want = guarded_call(ex, x, r.w, good, r.pos, 0)
         for fill in (0, 255):
             assert torch.equal(guarded_call(ex, x, r.w, bad, r.pos, fill), want), values
+
+
+@pytest.mark.parametrize("n,d", [(3, 64), (30, 64), (600, 64), (3000, 512)])
+def test_places_in_no_experts_rows_add_nothing(cuda_device, n, d):
+    """Bounds that leave rows out at either end: on every path a token's sum is
+    over the places that an expert has, whatever the workspace held."""
+    rng = np.random.default_rng(6)
+    f, e, k = 128, 3, 2
+    ex = Experts(rng, e, d, f, cuda_device)
+    x = tokens(rng, n, d, torch.float32).to(cuda_device)
+    r = sge.moe_route_fwd(torch.randn(n, e, device=cuda_device), k)
+    rows = n * k
+    pos, w, x64 = r.pos.cpu().numpy(), to_f64(r.w), x.cpu().numpy()
+    for values in ([rows // 4, rows // 2, rows // 2, 3 * rows // 4], [0, 1, 1, 1], [rows] * 4, [0] * 4,
+                   [rows // 2, 0, rows // 3, rows // 2 + 1]):
+        bounds, ascending = as_bounds(values, rows, cuda_device)
+        want, mag = np.zeros((n, d)), np.zeros((n, d))
+        lo = ascending.tolist()
+        for i in range(e):
+            t, j = np.nonzero((pos >= lo[i]) & (pos < lo[i + 1]))
+            if len(t):
+                z, m = ex.block(i, x64[t])
+                np.add.at(want, t, w[t, j][:, None] * z)
+                np.add.at(mag, t, w[t, j][:, None] * m)
+        for fill in (0, 255):
+            y = guarded_call(ex, x, r.w, bounds, r.pos, fill)
+            assert_close(y, want, mag, f, torch.float32)

@@ -253,11 +253,6 @@ struct FfnPlan {
   size_t xq, sx, hq, hs, z, total;  // workspace offsets
 };
 
-using GateUpPair = I8Shape<128, 2, 2, 1, true, true, false, 0>;
-using GateUpOne = I8Shape<128, 2, 2, 1, false, true, false, 0>;
-using DownPair = I8Shape<256, 1, 2, 2, true, true, true, 4096>;
-using DownOne = I8Shape<128, 1, 4, 2, false, true, true, 4096>;
-
 static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, bool routed) {
   FfnPlan p = {};
   p.rows = routed ? n * k : n;

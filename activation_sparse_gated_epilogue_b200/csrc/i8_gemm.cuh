@@ -76,6 +76,12 @@ struct I8Shape {
   static_assert(!PER_BLOCK || STAGES >= NACC, "stages");
 };
 
+// The products of the gated feed-forward block.
+using GateUpPair = I8Shape<128, 2, 2, 1, true, true, false, 0>;
+using GateUpOne = I8Shape<128, 2, 2, 1, false, true, false, 0>;
+using DownPair = I8Shape<256, 1, 2, 2, true, true, true, 4096>;
+using DownOne = I8Shape<128, 1, 4, 2, false, true, true, 4096>;
+
 struct I8Problem {
   int rows;    // rows of A
   int n;       // output columns of a group (rows of B per group)
@@ -549,6 +555,9 @@ __global__ void __launch_bounds__(Shape::THREADS, 1)
         release();
       }
     }
+    // every scale that is used has been waited for; a warp that gives up leaves
+    // copies to its slots in flight
+    if constexpr (PER_BLOCK) asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
   tc_fence_before();

@@ -28,12 +28,26 @@ struct EpiCountTiles {
   }
 };
 
-// The same for the 8-bit engine's epilogue interface.
+// The same for the 8-bit engine's epilogue interfaces: whole sums, and block by
+// block with a scale for each row and 128 of k.
 struct EpiCountI8 {
   int* tiles_done;
+  const float* scales;  // [k / 128][rows]
+  int64_t rows;
   template <int COLS>
   __device__ __forceinline__ void run(const I8Out& o, int) const {
     if (o.lane == 0) atomicAdd(tiles_done, 1);
+  }
+  __device__ __forceinline__ const float* block_scales(const I8Out& o) const {
+    return scales + (o.row < rows ? o.row : rows - 1);
+  }
+  __device__ __forceinline__ int64_t scale_pitch() const { return rows; }
+  template <int COLS>
+  __device__ __forceinline__ void store(const I8Out& o, const float (&sum)[COLS], int) const {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) s += sum[j];
+    if (o.lane == 0) atomicAdd(tiles_done, s == 0.0f ? 1 : 2);
   }
 };
 
@@ -43,7 +57,8 @@ static int i8_wait_timeout(const void* a, const void* b, int64_t m, int64_t n, i
                            int32_t* diag, cudaStream_t st) {
   const I8Problem p{static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), 1, 1, nullptr};
   I8Maps maps;
-  int rc = make_i8_maps<Shape>(&maps, p, static_cast<const int8_t*>(a), k, static_cast<const int8_t*>(b), nullptr, k);
+  const int8_t* b0 = static_cast<const int8_t*>(b);
+  int rc = make_i8_maps<Shape>(&maps, p, static_cast<const int8_t*>(a), k, b0, Shape::NB == 2 ? b0 : nullptr, k);
   if (!rc) rc = make_tmap_i8(&maps.b0, b, n, k, k, Shape::B_ROWS / 2);
   if (rc) return rc;
   return launch_i8_gemm<Shape>(maps, p, epi, diag, st, "selftest (8-bit engine)");
@@ -61,11 +76,18 @@ extern "C" int sge_selftest_wait_timeout(int pair, const void* a, const void* b,
     return fail(SGE_ERR_ARG, "sge_selftest_wait_timeout: bad arguments");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   EpiCountTiles epi{tiles_done};
-  if (pair == 2 || pair == 3) {  // the 8-bit engine: single CTA, CTA pair
-    if (k % 16) return fail(SGE_ERR_ARG, "sge_selftest_wait_timeout: bad arguments");
-    const EpiCountI8 e8{tiles_done};
-    return pair == 2 ? i8_wait_timeout<I8Shape<128, 1, 2, 1, false, false, false, 0>>(a, b, m, n, k, e8, diag, st)
-                     : i8_wait_timeout<I8Shape<256, 1, 2, 2, true, false, false, 0>>(a, b, m, n, k, e8, diag, st);
+  if (pair >= 2) {  // the 8-bit engine
+    if (pair > 7 || k % 16) return fail(SGE_ERR_ARG, "sge_selftest_wait_timeout: bad arguments");
+    // a's bytes as block scales (copied, not used): [k / 128][m] floats fit in its m x k
+    const EpiCountI8 e8{tiles_done, static_cast<const float*>(a), m};
+    switch (pair) {
+      case 2: return i8_wait_timeout<I8Shape<128, 1, 2, 1, false, false, false, 0>>(a, b, m, n, k, e8, diag, st);
+      case 3: return i8_wait_timeout<I8Shape<256, 1, 2, 2, true, false, false, 0>>(a, b, m, n, k, e8, diag, st);
+      case 4: return i8_wait_timeout<GateUpOne>(a, b, m, n, k, e8, diag, st);
+      case 5: return i8_wait_timeout<GateUpPair>(a, b, m, n, k, e8, diag, st);
+      case 6: return i8_wait_timeout<DownOne>(a, b, m, n, k, e8, diag, st);
+      default: return i8_wait_timeout<DownPair>(a, b, m, n, k, e8, diag, st);
+    }
   }
   CUtensorMap ma, mb;
   if (pair) {

@@ -14,8 +14,10 @@
  * its loads in flight, frees its tensor memory and returns.  No tile reaches
  * the epilogue: tiles_done (device int32, caller-zeroed) stays 0.  The call
  * takes well under a second and leaves the context usable.
- * pair = 2 and 3: the same with the 8-bit engine (single CTA, CTA pairs), which
- * reads the buffers as m x k and n x k bytes (k % 16 == 0).
+ * pair = 2 .. 7: the same with the 8-bit engine, which reads the buffers as
+ * m x k and n x k bytes (k % 16 == 0): 2 and 3 one product (single CTA, CTA
+ * pairs), 4 and 5 the gate and up products, 6 and 7 the down product block by
+ * block, whose copies of the block scales are in flight when the wait runs out.
  *   a [m][k], b [n][k]  bf16 device buffers (contents unused), 16-byte aligned
  *   diag  int32[4] device, caller-zeroed; tiles_done int32[1] device
  * Returns SGE_OK once launched; SGE_ERR_ARG for bad sizes or pointers.

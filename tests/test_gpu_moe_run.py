@@ -207,3 +207,28 @@ def test_bounded_wait_of_the_8_bit_engine_runs_out(cuda_device, pair):
     assert int(diag[3]) & 1 and int(tiles) == 0
     y, want, mag, parts = run_experts(cuda_device, 300, 128, 256, 3, 2, torch.float32)
     assert_close(y, want, mag, 256, torch.float32, parts)
+
+
+@pytest.mark.parametrize("pair", [4, 5, 6, 7])
+def test_bounded_waits_of_the_blocks_products_run_out(cuda_device, pair):
+    """The same for the shapes of the feed-forward block: two B loads a stage
+    (4, 5: single CTA, pairs), and the block-by-block sums (6, 7), whose epilogue
+    waits on the stages and has copies of its scales in flight."""
+    st = _selftest()
+    m, n, k = 512, 512, 2048
+    a = torch.zeros(m, k, dtype=torch.int8, device=cuda_device)
+    b = torch.zeros(n, k, dtype=torch.int8, device=cuda_device)
+    diag = sge.new_diag(cuda_device)
+    tiles = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    stream = ctypes.c_void_p(torch.cuda.current_stream(cuda_device).cuda_stream)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    assert st.sge_selftest_wait_timeout(pair, ctypes.c_void_p(a.data_ptr()), ctypes.c_void_p(b.data_ptr()), m, n, k,
+                                        ctypes.c_void_p(diag.data_ptr()), ctypes.c_void_p(tiles.data_ptr()),
+                                        stream) == 0
+    torch.cuda.synchronize()
+    assert time.perf_counter() - t0 < 5.0
+    assert int(diag[3]) & 1 and int(tiles) == 0
+    for tokens_n, d, f in ((300, 128, 1280), (3000, 512, 1280)):     # single CTAs, pairs
+        y, want, mag, _ = run_experts(cuda_device, tokens_n, d, f, 3, 2, torch.float32)
+        assert_close(y, want, mag, f, torch.float32)

@@ -17,7 +17,8 @@
 // kRouteBlocks values per expert from L2) and walks its rows in order,
 // so an assignment's place follows from sums of integers in a fixed order
 // and equals a stable sort's.  Probability sums are added in a fixed order
-// too (32 bits within a block, 64 across blocks): the same bits every run.
+// too (32 bits over at most kFoldRows rows and within a block, 64 beyond): the
+// same bits every run.
 // Latency bounds small batches (one token of 64 experts: 6.3 us), instructions
 // large ones (16384 x 256, k = 8: about 560 a row, 14 us to choose, 8 us to place,
 // 5 us for the gradient).
@@ -30,6 +31,10 @@ namespace sge {
 constexpr int kRouteThreads = 1024, kRouteWarps = 32;
 constexpr int kRouteBlocks = 148;  // most blocks of a call: one per SM
 constexpr int kMaxExperts = 256, kMaxTopK = 16;
+// Rows whose probabilities a warp adds in 32 bits: longer runs (more than 64 *
+// 32 * 148 tokens) go to 64-bit sums in shared memory every so many rows.  A
+// warp's 3543 rows of 16777216 tokens alone were off by 588 roundings.
+constexpr int kFoldRows = 64;
 
 struct RouteArgs {
   const uint8_t* mask;  // [n] or null
@@ -213,9 +218,11 @@ SGE_DEV uint32_t top_k(const float (&l)[V], int K, int lane, int& my_id, float& 
   }
 }
 
-// Rows of block b, warp by warp: choose, weigh, count.
+// Rows of block b, warp by warp: choose, weigh, count.  psum: [kRouteWarps][E];
+// wide: the same in 64 bits, or null where no warp has more than kFoldRows rows.
 template <class T, int V, bool VEC>
-SGE_DEV void route_choose(const T* __restrict__ logits, const RouteArgs& a, int b, int* hist, float* psum) {
+SGE_DEV void route_choose(const T* __restrict__ logits, const RouteArgs& a, int b, int* hist, float* psum,
+                          double* wide) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = a.experts, K = a.top_k;
   const int64_t first = (static_cast<int64_t>(b) * kRouteWarps + warp) * a.rows_per_warp;
@@ -233,8 +240,22 @@ SGE_DEV void route_choose(const T* __restrict__ logits, const RouteArgs& a, int 
   float p[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) p[v] = 0.0f;
-  int live = 0;
+  const auto fold = [&](bool start) {  // a lane's cells are its own
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (lane * V + v >= E) continue;
+      double* cell = wide + warp * E + lane * V + v;
+      *cell = start ? 0.0 : *cell + p[v];
+      p[v] = 0.0f;
+    }
+  };
+  if (wide) fold(true);
+  int live = 0, run = 0;
   for (int64_t row = first; row < last; ++row) {
+    if (wide && run++ == kFoldRows) {
+      fold(false);
+      run = 1;
+    }
     float l[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) l[v] = next[v];
@@ -278,13 +299,20 @@ SGE_DEV void route_choose(const T* __restrict__ logits, const RouteArgs& a, int 
     }
   }
   if (lane == 0) atomicAdd(&hist[E], live);
+  if (wide) fold(false);
 #pragma unroll
   for (int v = 0; v < V; ++v)
     if (lane * V + v < E) psum[warp * E + lane * V + v] = p[v];
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kRouteThreads) {
     float s = 0.0f;
-    for (int w = 0; w < kRouteWarps; ++w) s += psum[w * E + e];
+    if (wide) {
+      double d = 0.0;
+      for (int w = 0; w < kRouteWarps; ++w) d += wide[w * E + e];
+      s = static_cast<float>(d);
+    } else {
+      for (int w = 0; w < kRouteWarps; ++w) s += psum[w * E + e];
+    }
     a.part_p[static_cast<int64_t>(b) * E + e] = s;
   }
   for (int e = threadIdx.x; e <= E; e += kRouteThreads)
@@ -420,12 +448,18 @@ SGE_DEV void route_place(const RouteArgs& a, int b, int* hist) {
   }
 }
 
+// Shared words of a block: counts and sums, or the places' [kRouteWarps][E + 1];
+// even, so that 64-bit sums may follow.
+__host__ __device__ constexpr int route_words(int experts) { return ((kRouteWarps + 1) * (experts + 1) + 1) & ~1; }
+
 template <class T, int V, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads, 1) route_choose_kernel(const T* logits, const RouteArgs a) {
   extern __shared__ __align__(16) int smem[];
   grid_dep_wait();
   grid_dep_launch();
-  route_choose<T, V, VEC>(logits, a, blockIdx.x, smem, reinterpret_cast<float*>(smem + a.experts + 1));
+  float* psum = reinterpret_cast<float*>(smem + a.experts + 1);
+  double* wide = reinterpret_cast<double*>(smem + route_words(a.experts));
+  route_choose<T, V, VEC>(logits, a, blockIdx.x, smem, psum, a.rows_per_warp > kFoldRows ? wide : nullptr);
 }
 
 __global__ void __launch_bounds__(kRouteThreads, 1) route_place_kernel(const RouteArgs a) {
@@ -446,7 +480,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_one_kernel(const T* lo
   a.part_p = s_sum;
   grid_dep_wait();
   grid_dep_launch();
-  route_choose<T, V, VEC>(logits, a, 0, smem, reinterpret_cast<float*>(smem + a.experts + 1));
+  route_choose<T, V, VEC>(logits, a, 0, smem, reinterpret_cast<float*>(smem + a.experts + 1), nullptr);
   __syncthreads();
   route_place(a, 0, smem);
 }
@@ -569,15 +603,21 @@ static int route_blocks(int64_t n) {
 template <class T, int V, bool VEC>
 static int route_fwd_as(const void* logits, RouteArgs& a, cudaStream_t st) {
   const T* l = static_cast<const T*>(logits);
-  const size_t smem = static_cast<size_t>(kRouteWarps + 1) * (a.experts + 1) * 4;
+  const size_t smem = static_cast<size_t>(route_words(a.experts)) * 4;
   const void* last = a.blocks == 1 ? reinterpret_cast<const void*>(route_one_kernel<T, V, VEC>)
                                    : reinterpret_cast<const void*>(route_place_kernel);
   int rc = set_smem_limit(last, static_cast<int>(smem));  // with its static share it may pass 48 KB
   if (rc) return rc;
   if (a.blocks == 1)
     return launch_pdl(route_one_kernel<T, V, VEC>, dim3(1), dim3(kRouteThreads), smem, st, "moe_route_fwd", l, a);
-  rc = launch_pdl(route_choose_kernel<T, V, VEC>, dim3(a.blocks), dim3(kRouteThreads), smem, st,
-                            "moe_route_fwd (choose)", l, a);
+  size_t choose_smem = smem;
+  if (a.rows_per_warp > kFoldRows) {
+    choose_smem += static_cast<size_t>(kRouteWarps) * a.experts * 8;
+    rc = set_smem_limit(reinterpret_cast<const void*>(route_choose_kernel<T, V, VEC>), static_cast<int>(choose_smem));
+    if (rc) return rc;
+  }
+  rc = launch_pdl(route_choose_kernel<T, V, VEC>, dim3(a.blocks), dim3(kRouteThreads), choose_smem, st,
+                  "moe_route_fwd (choose)", l, a);
   if (rc) return rc;
   return launch_pdl(route_place_kernel, dim3(a.blocks), dim3(kRouteThreads), smem, st, "moe_route_fwd (place)", a);
 }

@@ -265,3 +265,88 @@ def test_route_of_the_callers_own_tensors(cuda_device):
         sge.moe_route_fwd(logits, k, out=bad)
     with pytest.raises(ValueError, match="shape"):
         sge.moe_route_fwd(logits, k + 1, out=want)
+
+
+def route_wide(l, k, renorm, mask):
+    """route_np over whole tensors, for long batches (no NaN or +inf)."""
+    n, e = l.shape
+    l = l.double()
+    if mask is not None:
+        l = torch.where(mask[:, None] != 0, l, -torch.inf)
+    live = (l > -torch.inf).any(1)
+    p = torch.where(live[:, None], torch.softmax(l, 1), 0.0)
+    value, ids = torch.sort(l, dim=1, descending=True, stable=True)
+    there = value[:, :k] > -torch.inf
+    ids = torch.where(there, ids[:, :k], -1)
+    w = torch.where(there, p.gather(1, ids.clamp(min=0)), 0.0)
+    if renorm:
+        w = torch.where(there, w / w.sum(1, keepdim=True).clamp(min=1e-300), 0.0)
+    flat = ids.reshape(-1)
+    counts = torch.bincount(flat[flat >= 0], minlength=e)
+    offsets = torch.cat([counts.new_zeros(1), torch.cumsum(counts, 0)])
+    by = torch.sort(torch.where(flat >= 0, flat, e), stable=True)[1]
+    place = torch.arange(n * k, device=l.device)
+    there = place < offsets[-1]
+    pos = torch.full_like(by, -1)
+    pos[by] = torch.where(there, place, -1)
+    order = torch.where(there, by, -1)
+    n_live = live.sum()
+    f = counts.double() / counts.sum().clamp(min=1)
+    loss = e * (f * p.sum(0)).sum() / n_live.clamp(min=1)
+    return dict(ids=ids, w=w, counts=counts, offsets=offsets, pos=pos.view(n, k), order=order, loss=loss,
+                n_live=n_live), p, f
+
+
+# rows a warp: 5 (the places beyond the four that stay in registers), 9, 64, 65
+# and 64 + 64 + 1 (where the probability sums are folded)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,e,k,renorm", [(18945, 7, 1, True), (40000, 100, 16, False), (303104, 33, 2, True),
+                                          (303105, 64, 4, False), (606209, 5, 3, True), (20001, 256, 8, False)])
+def test_route_of_long_batches(cuda_device, dtype, n, e, k, renorm):
+    g = torch.Generator(device=cuda_device).manual_seed(n)
+    logits = torch.randn(n, e, generator=g, device=cuda_device) + torch.randn(1, e, generator=g, device=cuda_device)
+    logits[::11, : e // 2] = -torch.inf       # fewer experts, for some fewer than k
+    logits[5::1000] = -torch.inf              # none
+    logits = logits.to(dtype)
+    mask = (torch.rand(n, generator=g, device=cuda_device) < 0.9).to(torch.uint8)
+    want, p, f = route_wide(logits, k, renorm, mask)
+    got = sge.moe_route_fwd(logits, k, renorm=renorm, mask=mask)
+    for name in ("ids", "counts", "offsets", "pos", "order"):
+        assert torch.equal(getattr(got, name).long(), want[name]), name
+    assert int(got.n_live) == int(want["n_live"])
+    # as in check(): an fp32 subtraction (|l - max| <= 20 here), expf, the sum, division and product
+    assert float(logits[logits > -torch.inf].abs().max()) < 10
+    rel, tiny = (2 * (20 + 4) + 20) * U, 2.0 ** -120
+    assert bool(((got.w.double() - want["w"]).abs() <= rel * want["w"] + tiny).all())
+    # a probability sum: at most 64 rows and 32 warps in fp32, the rest in 64 bits
+    assert abs(float(got.loss) - float(want["loss"])) <= (rel + (64 + 32 + 2) * U) * float(want["loss"])
+    dw = torch.randn(n, k, generator=g, device=cuda_device)
+    dloss = torch.tensor([0.37], device=cuda_device)
+    dl = sge.moe_route_bwd(logits, got, dloss, dw, mask=mask).double()
+    there, at = want["ids"] >= 0, want["ids"].clamp(min=0)
+    dw64 = torch.where(there, dw.double(), 0.0)
+    share = (0.37 * e * f / want["n_live"]).expand(n, e)
+    live = (p.sum(1, keepdim=True) > 0).double()
+    added = torch.zeros_like(p).scatter_add_(1, at, dw64) if not renorm else torch.zeros_like(p)
+    dp = share * live + added
+    # dloss is an fp32 number, 0.37 within U
+    ref = p * (dp - (p * dp).sum(1, keepdim=True))
+    size = p * ((share * live + added.abs()) + (p * (share * live + added.abs())).sum(1, keepdim=True))
+    if renorm:
+        w = want["w"]
+        ref = ref.scatter_add(1, at, w * (dw64 - (w * dw64).sum(1, keepdim=True)))
+        size = size.scatter_add(1, at, w * (dw64.abs() + (w * dw64.abs()).sum(1, keepdim=True)))
+    out = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    assert bool(((dl - ref).abs() <= (2 * rel + 61 * U) * size + out * ref.abs() + tiny).all())
+
+
+@pytest.mark.parametrize("n,e", [(2 ** 24 + 3, 5), (2 ** 22 + 1, 7)])
+def test_route_loss_of_very_long_batches(cuda_device, n, e):
+    """Equal logits: every token takes expert 0 and the loss is 1.  Each p is
+    1 / e within two roundings, a sum of 64 of them within 64, every other sum
+    is in 64 bits (fp32 sums of a warp's 3543 rows were off by 588 roundings)."""
+    r = sge.moe_route_fwd(torch.zeros(n, e, device=cuda_device), 1)
+    assert r.counts.tolist() == [n] + [0] * (e - 1) and int(r.n_live) == n
+    assert torch.equal(r.pos.view(-1), torch.arange(n, device=cuda_device, dtype=torch.int32))
+    assert torch.equal(r.order, torch.arange(n, device=cuda_device, dtype=torch.int32))
+    assert abs(float(r.loss) - 1) <= (2 + 64 + 2) * U

@@ -772,7 +772,8 @@ def moe_route_bwd(logits: torch.Tensor, route: MoeRoute, dloss: Optional[torch.T
 
 def int8_ffn_workspace(n_tokens: int, d_model: int, d_ff: int, n_experts: int, top_k: int, dtype: torch.dtype,
                        device) -> torch.Tensor:
-    """Scratch for int8_ffn_fwd (n_experts = top_k = 1) and moe_int8_ffn_fwd."""
+    """Scratch for int8_ffn_fwd (n_experts = top_k = 1) and moe_int8_ffn_fwd, for
+    batches of at most n_tokens."""
     nbytes = library().int8_ffn_workspace_bytes(n_tokens, d_model, d_ff, n_experts, top_k, _DTYPES[dtype])
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 

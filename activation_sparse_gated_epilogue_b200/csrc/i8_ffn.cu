@@ -253,6 +253,8 @@ struct FfnPlan {
   size_t xq, sx, hq, hs, z, total;  // workspace offsets
 };
 
+constexpr int64_t kSplitTiles = 148, kMaxSplits = 16;  // of a split down product
+
 static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, bool routed) {
   FfnPlan p = {};
   p.rows = routed ? n * k : n;
@@ -274,9 +276,9 @@ static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, bool rout
     // least 4 blocks (512 hidden units) each, no part empty
     const int64_t groups = e < p.rows ? e : p.rows;  // experts that can have rows
     const int64_t tiles = (p.rows / kBM + groups) * ((d + DownOne::BN - 1) / DownOne::BN);
-    int64_t s = tiles ? 148 / tiles : 1;
+    int64_t s = tiles ? kSplitTiles / tiles : 1;
     if (s > kb / 4) s = kb / 4;
-    if (s > 16) s = 16;
+    if (s > kMaxSplits) s = kMaxSplits;
     if (s < 1) s = 1;
     const int64_t per = (kb + s - 1) / s;
     p.splits = static_cast<int>((kb + per - 1) / per);
@@ -297,6 +299,19 @@ static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, bool rout
   p.z = p.combine ? take(static_cast<size_t>(p.rows) * p.splits * d * 4) : 0;
   p.total = at;
   return p;
+}
+
+// Bytes that a batch of n tokens or fewer needs, so that a program's workspace
+// for its largest batch serves all: a smaller batch whose down product is split
+// may keep more partial results than n tokens do.  Its tiles (128 x 128, at least
+// the rows and columns of z) times its splits are at most kSplitTiles.
+static size_t ffn_workspace(int64_t n, int64_t d, int64_t f, int e, int k, bool routed) {
+  const FfnPlan p = ffn_plan(n, d, f, e, k, routed);
+  const size_t z = p.combine ? align256(static_cast<size_t>(p.rows) * p.splits * d * 4) : 0;
+  const size_t most = static_cast<size_t>(kSplitTiles) * kBM * DownOne::BN * 4;
+  const size_t all = align256(static_cast<size_t>(p.rows) * kMaxSplits * d * 4);
+  const size_t split = all < most ? all : most;
+  return p.total - z + (z > split ? z : split);
 }
 
 struct FfnArgs {
@@ -418,8 +433,8 @@ extern "C" size_t int8_ffn_workspace_bytes(int64_t n_tokens, int64_t d_model, in
                                            int dtype) {
   if (check_ffn_sizes("int8_ffn_workspace_bytes", n_tokens, d_model, d_ff, n_experts, top_k, dtype)) return 0;
   // int8_ffn_fwd and moe_int8_ffn_fwd both take it
-  const size_t routed = ffn_plan(n_tokens, d_model, d_ff, n_experts, top_k, true).total;
-  const size_t dense = ffn_plan(n_tokens, d_model, d_ff, n_experts, top_k, false).total;
+  const size_t routed = ffn_workspace(n_tokens, d_model, d_ff, n_experts, top_k, true);
+  const size_t dense = ffn_workspace(n_tokens, d_model, d_ff, n_experts, top_k, false);
   return n_experts > 1 || routed > dense ? routed : dense;
 }
 

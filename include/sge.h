@@ -562,7 +562,8 @@ int moe_route_bwd(const void* logits, const uint8_t* mask, int64_t n_tokens, int
  *
  * Results do not depend on scheduling.  The workspace (256-byte aligned,
  * int8_ffn_workspace_bytes for either call; n_experts = top_k = 1 for
- * int8_ffn_fwd) belongs to one call at a time.
+ * int8_ffn_fwd) belongs to one call at a time; that of n_tokens serves every
+ * batch of at most as many.
  * Errors: SGE_ERR_ARG for bad sizes, d % 8, F % 8, top_k > E, a workspace too
  * small; SGE_ERR_UNSUPPORTED for d > 131071, E > 256, top_k > 16, other
  * dtypes, N * top_k, E * F or E * d of 2^30 and more.

@@ -377,3 +377,27 @@ def test_binding_of_the_8_bit_operators_and_the_router_refuses_cpu_tensors():
                  lambda: sge.moe_int8_ffn_fwd(x, rows, rows, rows, route.w, route.offsets, route.pos)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+@pytest.mark.parametrize("d,f,e,k", [(2048, 8192, 1, 1), (2048, 2048, 16, 2), (1024, 1024, 32, 4), (136, 4096, 3, 2),
+                                     (2560, 10240, 1, 1), (64, 16384, 256, 8), (8, 8, 1, 1)])
+def test_workspace_of_a_batch_serves_every_smaller_one(lib, d, f, e, k):
+    """The largest need of any batch up to n, by the call's own check of the
+    workspace, is what the size query gives for n."""
+    p = ctypes.c_void_p(4096)
+
+    def too_small(n, nbytes):
+        code = (lib.moe_int8_ffn_fwd(p, p, p, p, p, p, p, p, p, p, p, n, d, f, e, k, sge.SGE_BF16, p, nbytes, None, None)
+                if e > 1 else lib.int8_ffn_fwd(p, p, p, p, p, p, p, p, n, d, f, sge.SGE_BF16, p, nbytes, None, None))
+        return code == 1 and b"workspace" in lib.sge_last_error()
+
+    sizes = list(range(1, 1100)) + list(range(1100, 9000, 41))
+    given = [lib.int8_ffn_workspace_bytes(n, d, f, e, k, sge.SGE_BF16) for n in sizes]
+    assert given == sorted(given)
+    for n, nbytes in zip(sizes, given):
+        # the message of a call that gets 0 bytes names its need
+        assert too_small(n, 0)
+        need = int(lib.sge_last_error().decode().split(",")[1].split()[0])
+        assert 0 < need <= nbytes
+    route = [lib.moe_route_workspace_bytes(n, max(e, 2)) for n in sizes]
+    assert route == sorted(route)

@@ -774,6 +774,8 @@ def int8_ffn_workspace(n_tokens: int, d_model: int, d_ff: int, n_experts: int, t
                        device) -> torch.Tensor:
     """Scratch for int8_ffn_fwd (n_experts = top_k = 1) and moe_int8_ffn_fwd, for
     batches of at most n_tokens."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
     nbytes = library().int8_ffn_workspace_bytes(n_tokens, d_model, d_ff, n_experts, top_k, _DTYPES[dtype])
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
@@ -820,9 +822,11 @@ def moe_int8_ffn_fwd(x: torch.Tensor, wg_q: Int8Rows, wu_q: Int8Rows, wd_t_q: In
     wg_q, wu_q and wd_t_q), each token's summed with its weights; w, offsets
     and pos are moe_route_fwd's."""
     index = _device_of(x, "x")
-    e, k = offsets.shape[0] - 1, w.shape[1]
-    if e < 1:
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("offsets must be [experts + 1]")
+    if w.dim() != 2:
+        raise ValueError("w must be [tokens][top_k]")
+    e, k = offsets.shape[0] - 1, w.shape[1]
     n, d, f, weights, y, workspace = _ffn_operands(x, index, wg_q, wu_q, wd_t_q, e, k, y, workspace, stream)
     _launch("moe_int8_ffn_fwd", index, stream, x.data_ptr(), *weights,
             _operand(w, "w", index, torch.float32, (n, k)),

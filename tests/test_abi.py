@@ -401,3 +401,9 @@ def test_workspace_of_a_batch_serves_every_smaller_one(lib, d, f, e, k):
         assert 0 < need <= nbytes
     route = [lib.moe_route_workspace_bytes(n, max(e, 2)) for n in sizes]
     assert route == sorted(route)
+
+
+def test_int8_ffn_workspace_refuses_other_dtypes(lib):
+    import torch
+    with pytest.raises(ValueError, match="dtype"):
+        sge.int8_ffn_workspace(8, 64, 128, 1, 1, torch.float16, "cpu")

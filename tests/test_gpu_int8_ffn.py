@@ -300,3 +300,16 @@ def test_places_in_no_experts_rows_add_nothing(cuda_device, n, d):
         for fill in (0, 255):
             y = guarded_call(ex, x, r.w, bounds, r.pos, fill)
             assert_close(y, want, mag, f, torch.float32)
+
+
+def test_refusals_are_value_errors(cuda_device):
+    ex = Experts(np.random.default_rng(4), 2, 64, 128, cuda_device)
+    x = torch.randn(4, 64, device=cuda_device)
+    r = sge.moe_route_fwd(torch.randn(4, 2, device=cuda_device), 1)
+    with pytest.raises(ValueError, match="dtype"):
+        sge.moe_int8_ffn_fwd(x.half(), *ex.dev, r.w, r.offsets, r.pos)
+    with pytest.raises(ValueError, match="w must"):
+        sge.moe_int8_ffn_fwd(x, *ex.dev, r.w.view(-1), r.offsets, r.pos)
+    for offsets in (r.offsets[0], r.offsets[:1], r.offsets[None]):
+        with pytest.raises(ValueError, match="offsets"):
+            sge.moe_int8_ffn_fwd(x, *ex.dev, r.w, offsets, r.pos)

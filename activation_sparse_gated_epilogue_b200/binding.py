@@ -715,7 +715,8 @@ class MoeRoute:
 
 
 def moe_route_workspace(n_tokens: int, n_experts: int, top_k: int, device) -> torch.Tensor:
-    """Scratch for moe_route_fwd (each block's counts and probability sums)."""
+    """Scratch for moe_route_fwd (each block's counts and probability sums), for
+    batches of at most n_tokens; the same for every top_k."""
     nbytes = library().moe_route_workspace_bytes(n_tokens, n_experts)
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
@@ -741,11 +742,12 @@ def moe_route_fwd(logits: torch.Tensor, top_k: int, renorm: bool = True, mask: O
     index, n, e, x, m = _logits_operands(logits, mask)
     if out is None:
         out = _allocate(stream, MoeRoute.empty, n, e, max(top_k, 0), logits.device)
-    out.renorm = bool(renorm)
+    renorm = bool(renorm)
     if workspace is None:
         workspace = _allocate(stream, moe_route_workspace, n, e, top_k, logits.device)
-    _launch("moe_route_fwd", index, stream, x, m, n, e, top_k, int(out.renorm), _dtype_code(logits),
+    _launch("moe_route_fwd", index, stream, x, m, n, e, top_k, int(renorm), _dtype_code(logits),
             *out._operands(index, n, e, top_k), _scratch(workspace, index), workspace.numel())
+    out.renorm = renorm  # a refused call leaves `out` as it was
     return out
 
 

@@ -350,3 +350,18 @@ def test_route_loss_of_very_long_batches(cuda_device, n, e):
     assert torch.equal(r.pos.view(-1), torch.arange(n, device=cuda_device, dtype=torch.int32))
     assert torch.equal(r.order, torch.arange(n, device=cuda_device, dtype=torch.int32))
     assert abs(float(r.loss) - 1) <= (2 + 64 + 2) * U
+
+
+def test_refused_route_leaves_its_output_as_it_was(cuda_device):
+    """The gradient after a refused call is that of the route that is there."""
+    logits = torch.randn(9, 6, device=cuda_device)
+    r = sge.moe_route_fwd(logits, 2, renorm=True)
+    dw = torch.randn(9, 2, device=cuda_device)
+    want = sge.moe_route_bwd(logits, r, dw=dw)
+    with pytest.raises(ValueError):
+        sge.moe_route_fwd(logits, 3, renorm=False, out=r)
+    with pytest.raises(ValueError):
+        sge.moe_route_fwd(logits.half(), 2, renorm=False, out=r)
+    with pytest.raises(sge.LibraryError, match="workspace"):
+        sge.moe_route_fwd(logits, 2, renorm=False, out=r, workspace=torch.empty(16, dtype=torch.uint8, device=cuda_device))
+    assert r.renorm and torch.equal(sge.moe_route_bwd(logits, r, dw=dw), want)

@@ -37,15 +37,14 @@ int check_launch(const char* what) {
 }
 
 int sm_count() {
-  static int cached[64] = {0};
+  static PerDevice cached;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (cached[dev] == 0) {
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  return cached.get(dev, [dev] {
     int n = 0;
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    cached[dev] = n > 0 ? n : 148;
-  }
-  return cached[dev];
+    return n > 0 ? n : 148;
+  });
 }
 
 // The dynamic shared-memory limit of each (device, kernel) is set once and

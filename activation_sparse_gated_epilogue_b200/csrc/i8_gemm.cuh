@@ -593,10 +593,10 @@ int make_i8_maps(I8Maps* m, const I8Problem& p, const int8_t* a, int64_t lda, co
 template <class Shape, class Epi>
 int i8_workers() {
   if constexpr (!Shape::PAIR) return sm_count();
-  static int cached[64] = {0};
+  static PerDevice cached;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count() / 2;
-  if (cached[dev] == 0) {
+  if (cudaGetDevice(&dev) != cudaSuccess) return sm_count() / 2;
+  return cached.get(dev, [] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (sm_count() / 2));
     cfg.blockDim = dim3(Shape::THREADS);
@@ -614,9 +614,8 @@ int i8_workers() {
       cudaGetLastError();
       n = sm_count() / 2;
     }
-    cached[dev] = n;
-  }
-  return cached[dev];
+    return n;
+  });
 }
 
 template <class Shape, class Epi>

@@ -7,6 +7,7 @@
 #include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "../../include/sge.h"
@@ -37,6 +38,25 @@ struct NvtxRange {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline size_t align256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+// A positive number of each device, made when first asked for.  Several threads
+// may make it at once (the same number), so the cells are atomic.
+class PerDevice {
+ public:
+  template <class Make>
+  int get(int dev, Make make) {
+    if (dev < 0 || dev >= 64) return make();
+    int v = cells_[dev].load(std::memory_order_relaxed);
+    if (v == 0) {
+      v = make();
+      cells_[dev].store(v, std::memory_order_relaxed);
+    }
+    return v;
+  }
+
+ private:
+  std::atomic<int> cells_[64] = {};
+};
 
 // Multiprocessor count of the current device (cached per device).
 int sm_count();

@@ -19,30 +19,32 @@ int launch_tc_gemm(const CUtensorMap& ma, const CUtensorMap& mb0, const CUtensor
                     static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), epi, diag);
 }
 
-// Number of CTA pairs that can be resident at once (cached per kernel).
+// Number of CTA pairs that can be resident at once (cached per kernel and device).
 template <class Shape, class Epi>
 int max_resident_pairs() {
-  static int cached = 0;
-  if (cached) return cached;
-  auto kern = tc_gemm_pair_kernel<Shape, Epi>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (sm_count() / 2));
-  cfg.blockDim = dim3(Shape::THREADS);
-  cfg.dynamicSmemBytes = Shape::SMEM_BYTES;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kern), &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    n = sm_count() / 2;
-  }
-  cached = n;
-  return n;
+  static PerDevice cached;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return sm_count() / 2;
+  return cached.get(dev, [] {
+    auto kern = tc_gemm_pair_kernel<Shape, Epi>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sm_count() / 2));
+    cfg.blockDim = dim3(Shape::THREADS);
+    cfg.dynamicSmemBytes = Shape::SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kern), &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = sm_count() / 2;
+    }
+    return n;
+  });
 }
 
 // `splits`: the K splits the epilogue asks for (Epi::splits), for the grid size.

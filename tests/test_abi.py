@@ -407,3 +407,37 @@ def test_int8_ffn_workspace_refuses_other_dtypes(lib):
     import torch
     with pytest.raises(ValueError, match="dtype"):
         sge.int8_ffn_workspace(8, 64, 128, 1, 1, torch.float16, "cpu")
+
+
+def test_numbers_kept_for_each_device_are_made_without_a_race(tmp_path):
+    """Threads that ask for one device's number at once, under the thread
+    sanitiser."""
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text("""
+#include <thread>
+#include <vector>
+#include "sge_host.h"
+int main() {
+  sge::PerDevice kept;
+  std::vector<std::thread> threads;
+  std::atomic<int> wrong{0};
+  for (int t = 0; t < 8; ++t)
+    threads.emplace_back([&] {
+      for (int dev = -1; dev < 66; ++dev)
+        for (int i = 0; i < 2; ++i)
+          if (kept.get(dev, [dev] { return dev + 100; }) != dev + 100) ++wrong;
+    });
+  for (auto& t : threads) t.join();
+  return wrong;
+}
+""")
+    csrc = os.path.join(ROOT, "activation_sparse_gated_epilogue_b200", "csrc")
+    made = subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=thread", "-I", csrc, "-I", "/usr/local/cuda/include",
+                           str(src), "-o", str(exe), "-ldl", "-pthread"], capture_output=True, text=True)
+    if "cannot find" in made.stderr and "tsan" in made.stderr:
+        pytest.skip("no thread sanitiser here")
+    assert made.returncode == 0, made.stderr[-2000:]
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    if "unexpected memory mapping" in run.stderr:
+        pytest.skip("the thread sanitiser cannot run here")
+    assert run.returncode == 0 and "data race" not in run.stderr, run.stderr[-2000:]

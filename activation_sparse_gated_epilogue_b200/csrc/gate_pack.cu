@@ -32,21 +32,6 @@ struct EpiTwell {
   int cap;
   int32_t* diag;
 
-  // r[jj] for a run-time jj in [0, 32) without local memory: a 5-level
-  // select tree over the 32 registers.
-  __device__ __forceinline__ static uint32_t pick(const uint32_t (&r)[32], int jj) {
-    uint32_t a[16], b[8], c4[4], d2[2];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) a[i] = (jj & 16) ? r[i + 16] : r[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = (jj & 8) ? a[i + 8] : a[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c4[i] = (jj & 4) ? b[i + 4] : b[i];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) d2[i] = (jj & 2) ? c4[i + 2] : c4[i];
-    return (jj & 1) ? d2[1] : d2[0];
-  }
-
   // Store the active columns of `m` (bits of r) as entries of tile `seg`,
   // local index = bit + idx_off; c counts every active column.
   __device__ __forceinline__ void emit(uint32_t m, const uint32_t (&r)[32], int& c, int64_t seg,
@@ -56,7 +41,7 @@ struct EpiTwell {
       m &= m - 1;
       if (ok && c < cap) {
         idx[seg * cap + c] = static_cast<uint8_t>(jj + idx_off);
-        val[seg * cap + c] = f32_to_bf16_bits(__uint_as_float(pick(r, jj)));
+        val[seg * cap + c] = f32_to_bf16_bits(__uint_as_float(select32(r, jj)));
       }
       ++c;
     }

@@ -143,7 +143,7 @@ struct EpiI8Twell {
           left &= left - 1;
           if (ok && c < cap) {
             idx[seg * cap + c] = static_cast<uint8_t>(in_tile + j);
-            val[seg * cap + c] = f32_to_bf16_bits(pick(v, part * 16 + j));
+            val[seg * cap + c] = f32_to_bf16_bits(select32(v, part * 16 + j));
           }
           ++c;
         }
@@ -154,19 +154,6 @@ struct EpiI8Twell {
       }
     }
     if (overflow && diag) atomicAdd(reinterpret_cast<int*>(diag + SGE_DIAG_OVERFLOW_TILES), overflow);
-  }
-
-  // v[j] for a run-time j without local memory: a 5-level select tree.
-  __device__ __forceinline__ static float pick(const float (&v)[32], int j) {
-    float a[16], b[8], c[4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) a[i] = (j & 16) ? v[i + 16] : v[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = (j & 8) ? a[i + 8] : a[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = (j & 4) ? b[i + 4] : b[i];
-    const float d0 = (j & 2) ? c[2] : c[0], d1 = (j & 2) ? c[3] : c[1];
-    return (j & 1) ? d1 : d0;
   }
 };
 

@@ -200,6 +200,22 @@ SGE_DEV uint16_t f32_to_bf16_bits(float v) {
   return *reinterpret_cast<uint16_t*>(&b);
 }
 
+// r[j] for a run-time j in [0, 32) without local memory: a 5-level select tree
+// over the 32 registers.
+template <class T>
+SGE_DEV T select32(const T (&r)[32], int j) {
+  T a[16], b[8], c[4], d[2];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = (j & 16) ? r[i + 16] : r[i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = (j & 8) ? a[i + 8] : a[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = (j & 4) ? b[i + 4] : b[i];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) d[i] = (j & 2) ? c[i + 2] : c[i];
+  return (j & 1) ? d[1] : d[0];
+}
+
 // Programmatic dependent launch.  grid_dep_wait: block until the grid this
 // one depends on has completed and its memory operations are visible (a
 // no-op when the grid was launched without the attribute); every kernel

@@ -159,9 +159,28 @@ struct EpiI8Twell {
 
 // --------------------------------------------------------------- dispatch
 
-// Batches of at most this many rows run on single-CTA 128-row tiles (the gate
-// of 2048 x 8192 at 256 / 257 tokens: 18 / 29 us there, 25 us at 257 on pairs).
-constexpr int64_t kSmallI8Rows = 256;
+// Whether single-CTA tiles (128 rows, bn columns) leave every SM at most one: the
+// product then takes the narrowest such tiles, else pairs of 256 x 256.  us of the
+// product alone, weights from HBM, tokens x d -> columns:
+//   int8_linear                    64 columns  128 columns  pairs
+//   256 x 2560 -> 1024                    9.9         10.7   14.7
+//   1024 x 2560 -> 1024                  10.0         10.8   14.4
+//   2048 x 2560 -> 1024                  15.3         10.9   14.3
+//   4096 x 2560 -> 1024                  26.0         16.9   15.1
+//   257 / 512 / 1024 x 2560 -> 2560  10.1 / 15.2 / 20.7  10.9 / 11.3 / 16.6  14.8 / 15.0 / 15.5
+//   128 / 256 / 257 x 2048 -> 8192   9.6 / 13.7 / 17.9  10.3 / 10.4 / 14.7  14.6 / 14.7 / 14.4
+//   32 / 129 x 2560 -> 10240         15.4 / 20.8  11.4 / 17.0  17.3 / 15.7
+//   4096 x 1024 -> 64                     5.7          6.0    7.4
+// (at d = 1024 two rounds of 128 columns still beat pairs: 4096 -> 1024 10.2
+// against 11.6; the rule does not look at d.)
+//   gate, 1% open                             128 columns  pairs
+//   2048 / 4096 x 2560 -> 1024                12.0 / 18.1  13.3 / 14.0
+//   512 / 1024 x 2560 -> 2560                 12.6 / 17.6  14.1 / 14.6
+//   256 / 257 x 2048 -> 8192                  12.1 / 15.9  14.0 / 13.5
+//   128 / 129 x 2560 -> 10240                 15.2 / 21.0  17.7 / 17.0
+static bool one_tile_each(int64_t n, int64_t m, int bn) {
+  return ((n + kBM - 1) / kBM) * ((m + bn - 1) / bn) <= sm_count();
+}
 
 template <class Shape, class Epi>
 static int i8_product(const int8_t* xq, int64_t ldx, const int8_t* wq, int64_t ldw, int64_t n, int64_t m,
@@ -183,13 +202,10 @@ static int linear(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* 
                       static_cast<int>(k));
   }
   const EpiI8Linear<T> epi{static_cast<T*>(y), sx, sw};
-  // 2048 x 8192, 128 / 256 / 257 tokens: 9.2 / 13.8 / 18.4 us on 64 columns a
-  // tile (more tiles for a batch of few rows), 9.9 / 10.2 / 15.0 us on 128,
-  // and 13.3 us at 257 on CTA pairs
-  if (n <= kBM)
+  if (one_tile_each(n, m, 64))
     return i8_product<I8Shape<64, 1, 2, 1, false, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st,
                                                                        "int8_linear");
-  if (n <= kSmallI8Rows)
+  if (one_tile_each(n, m, 128))
     return i8_product<I8Shape<128, 1, 2, 2, false, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st,
                                                                         "int8_linear");
   return i8_product<I8Shape<256, 1, 2, 2, true, false, false, 4096>>(xq, ldx, wq, ldw, n, m, k, epi, diag, st,
@@ -201,7 +217,7 @@ static int gate(const int8_t* xq, int64_t ldx, const float* sx, const int8_t* wq
                 int64_t n, int64_t f, int64_t k, int cap, uint8_t* count, uint8_t* idx, void* val,
                 int32_t* diag, cudaStream_t st) {
   const EpiI8Twell<T> epi{count, idx, static_cast<uint16_t*>(val), cap, diag, sx, sw};
-  if (n <= kSmallI8Rows)
+  if (one_tile_each(n, f, 128))
     return i8_product<I8Shape<128, 1, 2, 1, false, false, false, 0>>(xq, ldx, wq, ldw, n, f, k, epi, diag, st,
                                                     "twell_gate_pack_int8");
   return i8_product<I8Shape<256, 1, 2, 2, true, false, false, 0>>(xq, ldx, wq, ldw, n, f, k, epi, diag, st,

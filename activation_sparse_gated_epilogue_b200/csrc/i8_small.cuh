@@ -11,8 +11,11 @@
 namespace sge {
 
 constexpr int kSmallTokens = 8;  // of the feed-forward block, where experts leave each weight few of them
-// int8_linear: 2048 x 8192 took 4.0 / 4.9 / 10.8 us for 1 / 2 / 4 tokens here and
-// 8.8 us for any of these numbers on the tiles.
+// int8_linear, weights from HBM, us for 1 / 2 / 3 / 4 tokens here and for any of
+// them on the tiles: 2048 -> 64 2.6 / 3.4 / 4.2 / 4.9 and 7.5, 2048 -> 1024 3.1 /
+// 3.7 / 4.5 / 5.3 and 8.6, 2560 -> 2560 4.6 / 5.1 / 6.1 / 7.1 and 9.8, 2048 -> 8192
+// 4.2 / 4.9 / 9.2 / 10.9 and 9.3 (from L2 3.3 / 4.4 / 8.8 / 10.4 and 7.8).  Three
+// and four tokens lose at the widest: the limit is the number that wins at all of these.
 constexpr int kSmallLinear = 2;
 constexpr int kHGroup = 128;  // hidden units of the feed-forward block that share a scale
 
@@ -43,7 +46,8 @@ SGE_DEV uint4 load_weights(const int8_t* p) {
 // ------------------------------------------------------------- int8_linear
 
 // One warp per output channel, 16 bytes of its row a lane, four loads in
-// flight; NT tokens' rows come from L1.  1 x 2048 -> 8192: 4.0 us (4.2 TB/s).
+// flight; NT tokens' rows come from L1.  1 x 2048 -> 8192, one call after another:
+// 4.2 us with the weights from HBM (4.0 TB/s), 3.3 us from L2.
 template <class T, int NT>
 __global__ void __launch_bounds__(256) i8_linear_small_kernel(const int8_t* __restrict__ xq, int64_t ldx,
                                                               const float* __restrict__ sx,

@@ -264,3 +264,28 @@ def test_refusals(cuda_device):
         sge.int8_quant_rows(x.t())
     with pytest.raises(sge.LibraryError, match="tile"):
         sge.twell_gate_pack_int8(xq, sge.int8_quant_rows(torch.randn(96, 64, device=cuda_device)), 48, 48)
+
+
+# tiles of 128 rows on the 148 SMs: 64 columns while that gives every SM at most
+# one, 128 columns while those do, pairs beyond; on each, short and ragged sizes
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,d,m", [(1000, 300, 1100), (3, 64, 9472), (18900, 65, 33),          # 64 columns
+                                   (3, 64, 9473), (200, 129, 4801), (2000, 96, 1000),          # 128 columns
+                                   (700, 129, 3300), (257, 256, 6500), (19000, 65, 33), (5000, 100, 500)])  # pairs
+def test_linear_on_every_tile_shape(cuda_device, dtype, n, d, m):
+    test_linear_matches_the_exact_product(cuda_device, dtype, n, d, m)
+
+
+@pytest.mark.parametrize("tile,cap", [(16, 5), (128, 128)])
+@pytest.mark.parametrize("n,d,f", [(1300, 96, 1152), (2049, 96, 1280), (140, 257, 9600), (18944, 40, 128),
+                                   (18945, 40, 128)])
+def test_gate_pack_int8_on_every_tile_shape(cuda_device, tile, cap, n, d, f):
+    test_gate_pack_int8(cuda_device, tile, cap, n, d, f)
+
+
+def test_linear_longest_rows_of_the_lowest_integer_on_pairs(cuda_device):
+    n, d, m = 300, 131071, 6500
+    low = lambda r: sge.Int8Rows(torch.full((r, d + 1), -128, dtype=torch.int8, device=cuda_device),  # noqa: E731
+                                 torch.ones(r, device=cuda_device), d)
+    y = sge.int8_linear(low(n), low(m), torch.float32)
+    assert (y.double() == torch.tensor(128.0 * 128 * d).float().double().item()).all()

@@ -117,7 +117,7 @@ struct EpiI8Gated {
 };
 
 // Block sums scaled and added (in the engine), then the channel's scale.  8192 x
-// 8192 x 2048: 173 us, 1.6 POPS: two instructions for each of the 2 x 10^9 block
+// 8192 x 2048: 173 us, 1.6 POPS: two instructions for each of the 1.07 x 10^9 block
 // sums (conversion, multiply-add) keep the epilogue busier than the tensor pipe
 // (46%), and 256 tiles are 3.5 waves of 74 pairs.
 template <class T>
@@ -178,7 +178,8 @@ struct EpiI8Down {
 // branched around, so that the loads of several splits and places are in flight
 // together (with a branch before each it took 1.6 times as long).  8000 tokens
 // over 16 experts of 2048 x 2048, two a token: the block took 238 us with z in
-// bf16 and takes 251 us (131 MB more through HBM).  Sixteen columns a lane spill
+// bf16 and takes 253 us (131 MB more through HBM; this kernel alone 34 us, 131 MB
+// read).  Sixteen columns a lane spill
 // at four blocks per SM (64 registers): 1-3% more of the block at 2048 to 12000
 // tokens over 8 to 32 experts.
 template <class T>
@@ -259,9 +260,10 @@ static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, bool rout
   FfnPlan p = {};
   p.rows = routed ? n * k : n;
   // A few tokens whose quantised rows fit a block's shared memory, at most two
-  // for each expert that can have any: 2048 x 8192 without experts took 20 / 24
-  // / 31 us for 1 / 2 / 4 tokens there and 28 us on tiles; 32 experts of 1024 x
-  // 1024, 4 of them a token, 30 us for 8 tokens and 40 us on tiles.
+  // for each expert that can have any: 2048 x 8192 without experts took 18 / 21
+  // / 31 us for 1 / 2 / 4 tokens there and 28 to 31 us on tiles, weights in L2 (20 /
+  // 23 us for 1 / 2, 34 on tiles, from HBM); 32 experts of 1024 x 1024, 4 of them a
+  // token, 28 us for 8 tokens and 39 us for 9 on tiles (30 and 45 from HBM).
   p.small = n <= kSmallTokens && p.rows <= 2 * (e < p.rows ? e : p.rows) && kSmallTokens * round16(d) <= 128 * 1024;
   // CTA pairs (256-row, 256-column tiles) when an expert has rows for more than
   // two of them on average and the down product's tiles fill most of the 74

@@ -174,8 +174,9 @@ SGE_DEV int used_experts(const SmallFfn& a, int rows, uint8_t* list, uint8_t* bo
 // Gate and up projections, h and its quantisation: one block per used expert
 // and group of 128 hidden units, 16 warps of 8 units.  The block quantises its
 // tokens' rows itself (a launch less).  NT: rows of an expert at a time.  With
-// the kernel below 18.7 us for one token of 2048 x 8192 (50 MB of weights), 10.8
-// us for one over four of 32 experts of 1024 x 1024.
+// the kernel below 19.8 us for one token of 2048 x 8192 (50 MB of weights) with the
+// weights from HBM, 18.1 from L2; 11.4 and 10.6 us for one over four of 32 experts
+// of 1024 x 1024.
 template <class T, int NT>
 __global__ void __launch_bounds__(512, 1) i8_small_up_kernel(const T* __restrict__ x, const SmallFfn a) {
   extern __shared__ __align__(16) int8_t s_x[];  // [NT][ldx]

@@ -254,7 +254,10 @@ struct FfnPlan {
   size_t xq, sx, hq, hs, z, total;  // workspace offsets
 };
 
-constexpr int64_t kSplitTiles = 148, kMaxSplits = 16;  // of a split down product
+// Of a split down product.  This and the plan's other bounds are numbers of this
+// GPU's 148 SMs, not of the current device: the size query for the workspace may
+// be made without one, and the call must come to the same plan.
+constexpr int64_t kSplitTiles = 148, kMaxSplits = 16;
 
 static FfnPlan ffn_plan(int64_t n, int64_t d, int64_t f, int e, int k, bool routed) {
   FfnPlan p = {};

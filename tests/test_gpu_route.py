@@ -301,7 +301,8 @@ def route_wide(l, k, renorm, mask):
 # and 64 + 64 + 1 (where the probability sums are folded)
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("n,e,k,renorm", [(18945, 7, 1, True), (40000, 100, 16, False), (303104, 33, 2, True),
-                                          (303105, 64, 4, False), (606209, 5, 3, True), (20001, 256, 8, False)])
+                                          (303105, 64, 4, False), (606209, 5, 3, True), (20001, 256, 8, False),
+                                          (303200, 256, 8, True), (310000, 131, 2, False)])
 def test_route_of_long_batches(cuda_device, dtype, n, e, k, renorm):
     g = torch.Generator(device=cuda_device).manual_seed(n)
     logits = torch.randn(n, e, generator=g, device=cuda_device) + torch.randn(1, e, generator=g, device=cuda_device)
